@@ -248,6 +248,126 @@ attn_status attn_cross_static_scratch(attn_mat q, attn_mat k_enc, attn_mat v_enc
 size_t attn_workspace_size(int32_t batch, int32_t t_q, int32_t t_kv, int32_t n_heads,
                            int32_t head_dim, int32_t mask_kind);
 
+/* ---------------------------------------------------------------------------
+ * Paged K/V cache. The pages of the sources describe one contiguous cache per
+ * sequence; these entry points serve the same decoder when many sequences of
+ * unlike lengths share one pool of K/V pages: writing a chunk's rows, attention
+ * of the chunk over the cache, the attention weight each slot has received, and
+ * shrinking the cache to its heaviest slots.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * K and V pools of num_pages * page_size rows; row p * page_size + s is slot s
+ * of page p and holds n_kv_heads * 64 fp16 values. Slot j of sequence b lies in
+ * page table[b * pages_per_seq + j / page_size], at j % page_size. An entry
+ * outside [0, num_pages) is a hole: its slots hold nothing and no query row
+ * sees them (pages behind a window may be given back that way). kv_lens[b] is
+ * the number of slots of sequence b in use, the new tokens included; it is
+ * clamped to [0, pages_per_seq * page_size] on the device. Entries behind a
+ * sequence's last used slot are not read, and what the pool holds in slots
+ * that no query row sees (behind the end, outside the window) may be anything,
+ * NaN included.
+ *   page_size  16, 32, 64, 128 or 256
+ *   k, v       may be column views of one buffer; num_pages * page_size and
+ *              batch * pages_per_seq * page_size below 2^31
+ */
+typedef struct {
+  attn_mat k, v;
+  const int32_t *table;    /* device pointer, [batch, pages_per_seq] int32, 4-byte aligned */
+  int32_t *kv_lens;        /* device pointer, [batch] int32, 4-byte aligned (written only as
+                              attn_paged_evict's destination) */
+  int32_t num_pages, page_size, pages_per_seq, n_kv_heads;
+} attn_paged_kv;
+
+/*
+ * Which slots a query row sees. With Q valid rows (q_lens[b], or t_q) and KV
+ * slots in use, row i sits at position p_i = i + KV - Q, as in attn_mask, and
+ * sees slot j iff i < Q, j < KV, j is not in a hole,
+ *   and if causal, j <= p_i,
+ *   and if window > 0, |p_i - j| < window or j < first.
+ * `first` (0 without a window) keeps the first tokens of a sequence visible
+ * after they have left the window.
+ */
+typedef struct {
+  int32_t window;          /* >= 0; 0: no window */
+  int32_t first;           /* >= 0; 0 when window is 0 */
+  int32_t causal;          /* 0 or 1 */
+  const int32_t *q_lens;   /* optional: device pointer, [batch] int32; clamped to [0, t_q] */
+} attn_paged_mask;
+
+/*
+ * attn_paged_append -- writes a chunk's K and V rows into their slots
+ * Row b * t_new + i of k_new and v_new (i < Q) goes to slot i + KV - Q of
+ * sequence b, where KV = kv_lens[b] already counts the chunk. Rows whose slot is
+ * negative or lies in a hole are dropped.
+ *   k_new, v_new [batch*t_new, n_kv_heads*64] fp16 (views of a packed
+ *   projection will do); must not overlap the pools.
+ * Two sequences whose tables share a page must not both write to it.
+ */
+attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cache, int32_t batch, int32_t t_new,
+                              const int32_t *q_lens, attn_stream_t stream);
+
+/*
+ * attn_paged -- attention of a chunk of new tokens over a paged cache
+ *   o_i = sum_{j in A_i} e^{s_ij} v_j / D_i,  D_i = sum_{j in A_i} e^{s_ij} [+ e^{sinks[h]}],
+ *   s_ij = scale * <q_i, k_j>,  lse_i = ln D_i              per query head h
+ * Query head h reads K/V head h / (n_heads / n_kv_heads); n_heads must be a
+ * multiple of n_kv_heads, with at most 32 query heads per K/V head.
+ *   q, out   [batch*t_q, n_heads*64] fp16; out must not overlap q or the pools
+ *   sinks    [n_heads] fp32 or NULL, as in attn_forward_sinks
+ *   lse      [batch*t_q, n_heads] fp32 or NULL
+ * A row that sees nothing (padding rows i >= Q too) is zero with lse = -inf.
+ * Precision as in attn_forward: fp32 scores, max, sum and output, softmax
+ * weights rounded to fp16 for the value product, the output rounded once.
+ * workspace: at least attn_paged_workspace_size(...) bytes, 16-byte aligned;
+ * NULL or a smaller one returns ATTN_ERR_INVALID. Calls that may run at the
+ * same time need a workspace each. The result does not depend on timing.
+ */
+attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                       attn_paged_mask mask, const float *sinks, float scale, attn_mat out, float *lse,
+                       void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* Bytes of workspace attn_paged needs for these sizes on the current device (0 for invalid sizes). */
+size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, int32_t n_kv_heads);
+
+/*
+ * attn_paged_weights -- the attention weight each slot receives from a chunk
+ *   w_out[b, j] = w_in[b, j] + sum_{i, h : j in A_i} e^{s_ij - lse_ih}
+ * with attn_paged's s, A_i and lse (a row with lse = -inf has no weight). The
+ * sums are fp32, added in a fixed order.
+ *   lse    [batch*t_q, n_heads] fp32
+ *   w_in   [batch, pages_per_seq*page_size] fp32, or NULL for zeros
+ *   w_out  the same shape; w_in itself, or not overlapping it
+ */
+attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                               attn_paged_mask mask, const float *lse, float scale, const float *w_in, float *w_out,
+                               attn_stream_t stream);
+
+/*
+ * attn_paged_evict -- shrinks each sequence to at most `budget` slots
+ * Of the slots in use that lie in no hole, those below `first` and the last
+ * `recent` below KV stay, then those of the largest w_in, ties to the lowest
+ * slot, up to budget in all (NaN counts as -inf). What stays keeps its order:
+ * kept slot n of sequence b moves to slot n of `dst` (rows of K and V), w_out[b, n]
+ * takes its weight, kept[b, n] its old slot; w_out is 0 and kept is -1 behind the
+ * last, and dst.kv_lens[b] is how many stayed. A row whose page in dst.table is
+ * out of range is not moved.
+ *   budget    >= 1, >= first + recent, at most dst's slots per sequence
+ *   dst       page_size and n_kv_heads as the source. Either other pools
+ *             (not overlapping the source's), or the same: then a page that is in
+ *             both tables must be at the same place in both, of the same
+ *             sequence, so table and dst.table may be one (in place).
+ *             dst.kv_lens may be the source's.
+ *   w_in      [batch, source slots per sequence] fp32
+ *   w_out     [batch, dst slots per sequence] fp32 or NULL; may be w_in when the two have
+ *             the same shape, else must not overlap it
+ *   kept      [batch, budget] int32
+ * Bytes are moved once; nothing else is allocated or kept.
+ */
+attn_status attn_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,
+                             const float *w_in, attn_paged_kv dst, float *w_out, int32_t *kept,
+                             attn_stream_t stream);
+
 /* Static, human-readable name of a status code. */
 const char *attn_status_string(attn_status status);
 

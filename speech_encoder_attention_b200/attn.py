@@ -12,13 +12,19 @@ The function names match the C entry points:
       (split=False sets ATTN_FLAG_NO_SPLIT)
     attn_forward with sinks=...                          -> attn_forward_sinks
     attn_cross(q, k_enc, v_enc, batch, t_q, t_enc, n_heads, out=None)   -> out
+and, on a paged K/V cache (PagedKV),
+    attn_paged_append(k_new, v_new, cache, batch, t_new)                -> None
+    attn_paged(q, cache, batch, t_q, n_heads, ...)                      -> out [, lse]
+    attn_paged_weights(q, cache, lse, batch, t_q, n_heads, weights=...) -> weights
+    attn_paged_evict(cache, weights, budget, first, recent, dst=None)   -> kept, weights
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
-from typing import Optional
+from dataclasses import dataclass
+from typing import Any, Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libattn.so")
@@ -73,6 +79,28 @@ class AttnPlanInfo(ctypes.Structure):
     ]
 
 
+class AttnPagedKV(ctypes.Structure):
+    _fields_ = [
+        ("k", AttnMat),
+        ("v", AttnMat),
+        ("table", ctypes.c_void_p),
+        ("kv_lens", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("pages_per_seq", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+    ]
+
+
+class AttnPagedMask(ctypes.Structure):
+    _fields_ = [
+        ("window", ctypes.c_int32),
+        ("first", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("q_lens", ctypes.c_void_p),
+    ]
+
+
 # (name, restype, argtypes) of every exported entry point.
 SIGNATURES = {
     "attn_qkv_pack": (ctypes.c_int, [AttnMat, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -94,6 +122,18 @@ SIGNATURES = {
                                                  ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                                  ctypes.c_float, AttnMat, ctypes.c_void_p]),
     "attn_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 6),
+    "attn_paged_append": (ctypes.c_int, [AttnMat, AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.c_void_p, ctypes.c_void_p]),
+    "attn_paged": (ctypes.c_int, [AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, AttnPagedMask,
+                                  ctypes.c_void_p, ctypes.c_float, AttnMat, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_size_t, ctypes.c_void_p]),
+    "attn_paged_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "attn_paged_weights": (ctypes.c_int, [AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                          AttnPagedMask, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
+                                          ctypes.c_void_p, ctypes.c_void_p]),
+    "attn_paged_evict": (ctypes.c_int, [AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.c_void_p, AttnPagedKV, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p]),
     "attn_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "attn_debug_error_word": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
     "attn_debug_timeout_probe": (ctypes.c_int, [ctypes.c_int64, ctypes.c_void_p]),
@@ -303,6 +343,201 @@ def encoder_layer_attention(x, w_qkv, b_q, b_v, batch, t, n_heads, mask_kind=MAS
     qkv = attn_qkv_pack(x, w_qkv, b_q, b_v, out=qkv, stream=stream)
     return attn_forward(qkv[:, :d], qkv[:, d:2 * d], qkv[:, 2 * d:], batch, t, t, n_heads,
                         mask_kind=mask_kind, chunk_len=chunk_len, out=out, stream=stream)
+
+
+# ---------------------------------------------------------------------------
+# paged K/V cache
+# ---------------------------------------------------------------------------
+
+@dataclass
+class PagedKV:
+    """A paged K/V cache: pools k and v [num_pages * page_size, n_kv_heads * 64]
+    fp16 (column views of one buffer will do), table [batch, pages_per_seq] int32
+    (entries outside [0, num_pages) are holes) and lens [batch] int32, the slots
+    in use, new tokens included. Slot j of sequence b is row
+    table[b, j // page_size] * page_size + j % page_size."""
+    k: Any
+    v: Any
+    table: Any
+    lens: Any
+    page_size: int
+    n_kv_heads: int
+
+    @property
+    def slots(self) -> int:
+        """Slots per sequence that the table can address."""
+        return self.table.shape[1] * self.page_size
+
+
+def _dev_tensor(t, what: str, dtype, shape, device):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (there is no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the cache on {device}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} tensor")
+    return t.data_ptr()
+
+
+def _rows(t, what: str, rows: int, cols: int, device) -> AttnMat:
+    m = _mat(t)
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the cache on {device}")
+    if t.shape[0] != rows or t.shape[1] < cols:
+        raise ValueError(f"{what} must have {rows} rows of at least {cols} columns, got {list(t.shape)}")
+    return m
+
+
+def _paged_kv(cache: PagedKV, batch: int) -> AttnPagedKV:
+    import torch
+    if cache.page_size not in (16, 32, 64, 128, 256):
+        raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {cache.page_size}")
+    k, v = _mat(cache.k), _mat(cache.v)
+    dev = cache.k.device
+    if cache.v.device != dev or cache.v.shape[0] != cache.k.shape[0]:
+        raise ValueError("the K and V pools must lie on one device and have as many rows")
+    rows, cols = cache.k.shape[0], cache.n_kv_heads * HEAD_DIM
+    if rows == 0 or rows % cache.page_size or min(cache.k.shape[1], cache.v.shape[1]) < cols:
+        raise ValueError(f"the pools must hold whole pages of {cache.page_size} rows of {cols} columns")
+    if cache.table.dim() != 2:
+        raise ValueError("table must be a [batch, pages_per_seq] int32 tensor")
+    table = _dev_tensor(cache.table, "table", torch.int32, (batch, cache.table.shape[1]), dev)
+    lens = _dev_tensor(cache.lens, "lens", torch.int32, (batch,), dev)
+    return AttnPagedKV(k, v, table, lens, rows // cache.page_size, cache.page_size, cache.table.shape[1],
+                       cache.n_kv_heads)
+
+
+def _paged_mask(window, first, causal, q_lens, batch, device) -> AttnPagedMask:
+    import torch
+    ptr = 0 if q_lens is None else _dev_tensor(q_lens, "q_lens", torch.int32, (batch,), device)
+    return AttnPagedMask(window, first, 1 if causal else 0, ptr)
+
+
+class _On:
+    """The tensors' device and the call's stream as the current ones, so that
+    what is allocated and launched belongs to them."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = [torch.cuda.device(device)]
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the cache on {device}")
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return _stream_ptr()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def attn_paged_append(k_new, v_new, cache: PagedKV, batch, t_new, q_lens=None, stream=None) -> None:
+    """Writes a chunk's K and V rows ([batch*t_new, n_kv_heads*64] fp16, or column
+    views) into the slots at the end of each sequence; cache.lens already counts
+    them, q_lens ([batch] int32) says how many of the t_new rows are valid."""
+    lib = load_library()
+    kv = _paged_kv(cache, batch)
+    dev, cols = cache.k.device, cache.n_kv_heads * HEAD_DIM
+    kn, vn = _rows(k_new, "k_new", batch * t_new, cols, dev), _rows(v_new, "v_new", batch * t_new, cols, dev)
+    mask = _paged_mask(0, 0, True, q_lens, batch, dev)
+    with _On(dev, stream) as s:
+        _check(lib.attn_paged_append(kn, vn, kv, batch, t_new, mask.q_lens, s), "attn_paged_append")
+
+
+def paged_workspace_size(batch, t_q, n_heads, n_kv_heads) -> int:
+    return int(load_library().attn_paged_workspace_size(batch, t_q, n_heads, n_kv_heads))
+
+
+def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal=True, q_lens=None, sinks=None,
+               scale=DEFAULT_SCALE, out=None, return_lse=False, lse=None, workspace=None, stream=None):
+    """Attention of a chunk of new tokens (t_q = 1: a decode step) over a paged
+    cache; q [batch*t_q, >= n_heads*64] fp16. window and first limit what a row
+    sees to the last `window` slots and the `first` first ones (window=0: all).
+    Returns out, or (out, lse) with return_lse or lse given; lse is
+    [batch*t_q, n_heads] fp32, the log of each row's softmax denominator.
+    Without workspace one is allocated for the call."""
+    import torch
+    lib = load_library()
+    kv = _paged_kv(cache, batch)
+    dev, cols = cache.k.device, n_heads * HEAD_DIM
+    qm = _rows(q, "q", batch * t_q, cols, dev)
+    mask = _paged_mask(window, first, causal, q_lens, batch, dev)
+    sinks_ptr = 0 if sinks is None else _dev_tensor(sinks, "sinks", torch.float32, (n_heads,), dev)
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(batch * t_q, cols, dtype=torch.float16, device=dev)
+        if lse is None and return_lse:
+            lse = torch.empty(batch * t_q, n_heads, dtype=torch.float32, device=dev)
+        lse_ptr = 0 if lse is None else _dev_tensor(lse, "lse", torch.float32, (batch * t_q, n_heads), dev)
+        if workspace is None:
+            workspace = torch.empty(max(16, paged_workspace_size(batch, t_q, n_heads, cache.n_kv_heads)),
+                                    dtype=torch.uint8, device=dev)
+        elif workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, the cache on {dev}")
+        st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, float(scale),
+                            _rows(out, "out", batch * t_q, cols, dev), lse_ptr, _ptr(workspace),
+                            workspace.numel() * workspace.element_size(), s)
+        _check(st, "attn_paged")
+    return out if lse is None else (out, lse)
+
+
+def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, first=0, causal=True, q_lens=None,
+                       scale=DEFAULT_SCALE, weights=None, out=None, stream=None):
+    """What attn_paged's rows put on each slot, summed over rows and heads, added
+    to weights ([batch, cache.slots] fp32; None: zeros). lse is attn_paged's.
+    Returns out, a new tensor unless given; out=weights adds in place."""
+    import torch
+    lib = load_library()
+    kv = _paged_kv(cache, batch)
+    dev = cache.k.device
+    qm = _rows(q, "q", batch * t_q, n_heads * HEAD_DIM, dev)
+    mask = _paged_mask(window, first, causal, q_lens, batch, dev)
+    lse_ptr = _dev_tensor(lse, "lse", torch.float32, (batch * t_q, n_heads), dev)
+    shape = (batch, cache.slots)
+    w_in = 0 if weights is None else _dev_tensor(weights, "weights", torch.float32, shape, dev)
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=dev)
+        w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
+        st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, float(scale), w_in, w_out, s)
+        _check(st, "attn_paged_weights")
+    return out
+
+
+def attn_paged_evict(cache: PagedKV, weights, budget, first=0, recent=0, dst: Optional[PagedKV] = None, kept=None,
+                     weights_out=None, stream=None):
+    """Shrinks each sequence to its `first` first, `recent` last and heaviest
+    slots, `budget` in all, in order, at the front of dst (None: in place, in
+    cache's own pages; cache.lens is updated). Returns (kept, weights):
+    kept [batch, budget] int32 holds the old slot of each new one (-1 behind the
+    last), weights [batch, dst slots] the moved weights (0 behind the last).
+    dst.lens is written. Without weights_out a new tensor is returned;
+    weights_out=weights works in place when dst has as many slots."""
+    import torch
+    lib = load_library()
+    batch = cache.table.shape[0]
+    kv = _paged_kv(cache, batch)
+    dev = cache.k.device
+    if dst is None:
+        dst = cache
+    if dst.k.device != dev:
+        raise ValueError(f"dst is on {dst.k.device}, the cache on {dev}")
+    to = _paged_kv(dst, batch)
+    w_in = _dev_tensor(weights, "weights", torch.float32, (batch, cache.slots), dev)
+    with _On(dev, stream) as s:
+        if kept is None:
+            kept = torch.empty(batch, budget, dtype=torch.int32, device=dev)
+        if weights_out is None:
+            weights_out = torch.empty(batch, dst.slots, dtype=torch.float32, device=dev)
+        st = lib.attn_paged_evict(kv, batch, budget, first, recent, w_in, to,
+                                  _dev_tensor(weights_out, "weights_out", torch.float32, (batch, dst.slots), dev),
+                                  _dev_tensor(kept, "kept", torch.int32, (batch, budget), dev), s)
+        _check(st, "attn_paged_evict")
+    return kept, weights_out
 
 
 def debug_error_word(stream=None):

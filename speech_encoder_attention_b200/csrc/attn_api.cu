@@ -16,6 +16,10 @@
 
 #include "attn.h"
 #include "flash_attn.cuh"
+#include "paged_cache.cuh"
+#include "paged_common.cuh"
+#include "paged_step.cuh"
+#include "paged_weights.cuh"
 #include "qkv_gemm.cuh"
 #include "qkv_q8.cuh"
 #include "sm100_ptx.cuh"
@@ -127,6 +131,10 @@ attn_status device_info(DeviceInfo** out) {
                              sea::gemm::PairShape::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::q8::qkv_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::q8::SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(sea::pg::paged_step_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sea::pg::StepCfg<1>::SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(sea::pg::paged_step_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sea::pg::StepCfg<2>::SMEM_BYTES) != cudaSuccess ||
         !set_attention_smem<2>() || !set_attention_smem<4>())
       return ATTN_ERR_CUDA;
     d.num_sms = sms;
@@ -513,6 +521,8 @@ attn_status static_scratch(void** out) {
   return ATTN_OK;
 }
 
+#include "paged_host.cuh"
+
 }  // namespace
 
 extern "C" {
@@ -662,6 +672,35 @@ size_t attn_workspace_size(int32_t batch, int32_t t_q, int32_t t_kv, int32_t n_h
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != ATTN_OK) return 0;
   return plan_forward(batch, t_q, t_kv, n_heads, mask_kind, 0, dev->num_sms).ws_bytes;
+}
+
+attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cache, int32_t batch, int32_t t_new,
+                              const int32_t* q_lens, attn_stream_t stream) {
+  return launch_paged_append(k_new, v_new, cache, batch, t_new, q_lens, stream);
+}
+
+attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                       attn_paged_mask mask, const float* sinks, float scale, attn_mat out, float* lse,
+                       void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  return launch_paged(q, cache, batch, t_q, n_heads, mask, sinks, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, int32_t n_kv_heads) {
+  if (!valid_paged_heads(batch, t_q, n_heads, n_kv_heads)) return 0;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev) != ATTN_OK) return 0;
+  return plan_paged(t_q, n_heads / n_kv_heads, dev->num_sms).ws_bytes;
+}
+
+attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                               attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
+                               attn_stream_t stream) {
+  return launch_paged_weights(q, cache, batch, t_q, n_heads, mask, lse, scale, w_in, w_out, stream);
+}
+
+attn_status attn_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,
+                             const float* w_in, attn_paged_kv dst, float* w_out, int32_t* kept, attn_stream_t stream) {
+  return launch_paged_evict(cache, batch, budget, first, recent, w_in, dst, w_out, kept, stream);
 }
 
 const char* attn_status_string(attn_status status) {

@@ -1,0 +1,297 @@
+// paged_common.cuh -- what the kernels on a paged K/V cache share: the cache's
+// addressing, which slots a query row sees, and the split of the work.
+//
+// Slot j of sequence b lives in pool row table[b][j / page] * page + j % page;
+// a table entry outside [0, num_pages) is a hole, and the slots of a hole hold
+// nothing. KV = lens[b] counts the new tokens too: query row i of Q sits at
+// position p = i + KV - Q and sees
+//   j < KV, not in a hole, j <= p if causal, and with a window
+//   |p - j| < window or j < first.
+// Both ends of the window part and the end of the first part do not decrease
+// in i, so the slots that any row of a query tile sees are [lo, hi) and
+// [0, f), and the tile walks the 128-slot key tiles that meet them.
+#pragma once
+
+#include "sm100_ptx.cuh"
+
+namespace sea {
+namespace pg {
+
+constexpr int DH = 64;
+constexpr int BKV = 128;                      // slots per key tile
+constexpr int TILE_BYTES = BKV * DH * 2;      // one 128-slot x 64-column fp16 tile
+constexpr int GRANULE = 16;                   // smallest page: one bit of a tile's hole mask
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Geo {
+  int batch, t_q, n_heads, kv_heads, group;  // group = n_heads / kv_heads query heads share a K/V head
+  int tok_per_tile, q_tiles;                 // query tile: tok_per_tile tokens x group heads
+  int page_shift, pages_per_seq, num_pages;
+  int cap;                                   // slots the table can address
+  const int* table;
+  const int* kv_lens;
+  const int* q_lens;                         // may be null: every row is valid
+  int window, first, causal;                 // window 0: none
+};
+
+struct Seq {
+  int q, kv, off;
+};
+
+__device__ __forceinline__ Seq seq_of(const Geo& g, int b) {
+  Seq s;
+  s.kv = min(max(__ldg(g.kv_lens + b), 0), g.cap);
+  s.q = g.q_lens != nullptr ? min(max(__ldg(g.q_lens + b), 0), g.t_q) : g.t_q;
+  s.off = s.kv - s.q;
+  return s;
+}
+
+// What the row at position p sees: [lo, hi) and [0, f).
+struct RowSpan {
+  int lo, hi, f;
+};
+
+__device__ __forceinline__ RowSpan row_span(const Geo& g, const Seq& s, int p) {
+  const int end = max(0, g.causal ? min(s.kv, p + 1) : s.kv);
+  RowSpan r{0, end, 0};
+  if (g.window) {
+    r.lo = max(0, p - g.window + 1);
+    r.hi = max(0, min(end, p + g.window));
+    r.f = min(g.first, end);
+  }
+  return r;
+}
+
+// The key tiles of a query tile: k = 0 .. n-1 stands for tile k (k < n_first)
+// or t_lo + k - n_first.
+struct Span {
+  int tok0, ntok;       // valid tokens [tok0, tok0 + ntok) of the sequence's chunk
+  int lo, hi, f;        // union over the tile's rows
+  int n_first, t_lo, n;
+  __device__ __forceinline__ int tile(int k) const { return k < n_first ? k : t_lo + k - n_first; }
+};
+
+__device__ __forceinline__ Span span_of(const Geo& g, const Seq& s, int qt) {
+  Span u;
+  u.tok0 = qt * g.tok_per_tile;
+  u.ntok = min(g.tok_per_tile, s.q - u.tok0);
+  u.lo = u.hi = u.f = u.n_first = u.t_lo = u.n = 0;
+  if (u.ntok <= 0) {
+    u.ntok = 0;
+    return u;
+  }
+  const RowSpan a = row_span(g, s, u.tok0 + s.off);
+  const RowSpan z = row_span(g, s, u.tok0 + u.ntok - 1 + s.off);
+  u.lo = a.lo;
+  u.hi = z.hi;
+  u.f = z.f;
+  int t_hi = (u.hi + BKV - 1) / BKV;
+  u.t_lo = u.lo / BKV;
+  if (u.hi <= u.lo) {
+    u.lo = u.hi = 0;
+    t_hi = u.t_lo = 0;
+  }
+  u.n_first = (u.f + BKV - 1) / BKV;
+  if (t_hi > u.t_lo) u.n_first = min(u.n_first, u.t_lo);
+  u.n = u.n_first + t_hi - u.t_lo;
+  return u;
+}
+
+// ---------------------------------------------------------------------------
+// work split: the key tiles of all (sequence, K/V head, query tile) units in
+// one line, cut into equal shares, one per CTA. A unit whose tiles fall into
+// several shares leaves unnormalised partials in the workspace.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ int tiles_of_seq(const Geo& g, int b) {
+  const Seq s = seq_of(g, b);
+  int n = 0;
+  for (int qt = 0; qt < g.q_tiles; ++qt) n += span_of(g, s, qt).n;
+  return n;
+}
+
+// One warp: the tiles of all sequences before b (times K/V heads) and, with
+// b == batch, of all. Lanes take sequences; with many query tiles per
+// sequence they take query tiles.
+__device__ __forceinline__ long long tiles_before(const Geo& g, int b) {
+  const int lane = threadIdx.x & 31;
+  long long sum = 0;
+  if (g.q_tiles <= 4) {
+    for (int i = lane; i < b; i += 32) sum += tiles_of_seq(g, i);
+  } else {
+    for (int i = 0; i < b; ++i) {
+      const Seq s = seq_of(g, i);
+      for (int qt = lane; qt < g.q_tiles; qt += 32) sum += span_of(g, s, qt).n;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * g.kv_heads;
+}
+
+// Tiles of query tiles [0, qt) of one sequence (one warp).
+__device__ __forceinline__ int tiles_before_q(const Geo& g, const Seq& s, int qt) {
+  int sum = 0;
+  for (int i = threadIdx.x & 31; i < qt; i += 32) sum += span_of(g, s, i).n;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum;
+}
+
+// Tiles per CTA: an equal share, at least `least`.
+__device__ __forceinline__ long long share_of(long long total, int ctas, int least) {
+  const long long per = (total + ctas - 1) / ctas;
+  return per < least ? least : per;
+}
+
+// One CTA's share, unit by unit. Every warp of the CTA walks the same steps.
+struct Walk {
+  long long pos, end;   // tiles left: [pos, end)
+  long long begin;
+  int b, h, qt;
+  Seq s;
+  Span u;
+  int k0, k1;           // key tiles [k0, k1) of the unit u
+  bool whole;           // the unit's tiles are all here
+  int slot;             // partial slot of this share (0: its first unit, 1: a later one)
+};
+
+__device__ __forceinline__ void walk_cut(const Geo& g, Walk& w, int k0) {
+  w.k0 = k0;
+  const long long left = w.end - w.pos;
+  w.k1 = static_cast<int>(min(static_cast<long long>(w.u.n), k0 + left));
+  w.whole = k0 == 0 && w.k1 == w.u.n;
+  w.slot = w.pos == w.begin ? 0 : 1;
+}
+
+// One warp; returns false if the share is empty.
+__device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int cta, int ctas, int least) {
+  const int lane = threadIdx.x & 31;
+  const long long total = tiles_before(g, g.batch);
+  const long long per = share_of(total, ctas, least);
+  w.begin = w.pos = per * cta;
+  w.end = min(total, w.pos + per);
+  if (w.pos >= w.end) return false;
+  // the sequence that holds tile `pos`
+  long long base = 0;
+  int b = 0, seq_tiles = 0;
+  if (g.q_tiles <= 4) {
+    for (int b0 = 0; b0 < g.batch; b0 += 32) {
+      const int n = b0 + lane < g.batch ? tiles_of_seq(g, b0 + lane) : 0;
+      long long incl = static_cast<long long>(n) * g.kv_heads;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + incl > w.pos);
+      if (past) {
+        const int i = __ffs(past) - 1;
+        b = b0 + i;
+        seq_tiles = __shfl_sync(0xffffffffu, n, i);
+        base += __shfl_sync(0xffffffffu, incl, i) - static_cast<long long>(seq_tiles) * g.kv_heads;
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  } else {
+    for (b = 0; b < g.batch; ++b) {
+      seq_tiles = tiles_before_q(g, seq_of(g, b), g.q_tiles);
+      const long long n = static_cast<long long>(seq_tiles) * g.kv_heads;
+      if (base + n > w.pos) break;
+      base += n;
+    }
+  }
+  const long long in_seq = w.pos - base;
+  w.b = b;
+  w.s = seq_of(g, b);
+  w.h = static_cast<int>(in_seq / seq_tiles);
+  int rest = static_cast<int>(in_seq - static_cast<long long>(w.h) * seq_tiles);
+  // the query tile that holds it
+  int qt = 0;
+  for (int q0 = 0; q0 < g.q_tiles; q0 += 32) {
+    const int n = q0 + lane < g.q_tiles ? span_of(g, w.s, q0 + lane).n : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, incl > rest);
+    if (past) {
+      const int i = __ffs(past) - 1;
+      qt = q0 + i;
+      rest -= __shfl_sync(0xffffffffu, incl - n, i);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  w.qt = qt;
+  w.u = span_of(g, w.s, qt);
+  walk_cut(g, w, rest);
+  return true;
+}
+
+// The next unit of the share; false when the share is done. Any thread.
+__device__ __forceinline__ bool walk_next(const Geo& g, Walk& w) {
+  w.pos += w.k1 - w.k0;
+  if (w.pos >= w.end) return false;
+  do {
+    if (++w.qt == g.q_tiles) {
+      w.qt = 0;
+      if (++w.h == g.kv_heads) {
+        w.h = 0;
+        ++w.b;
+        w.s = seq_of(g, w.b);
+      }
+    }
+    w.u = span_of(g, w.s, w.qt);
+  } while (w.u.n == 0);
+  walk_cut(g, w, 0);
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// loads of one key tile (the producer warp)
+// ---------------------------------------------------------------------------
+
+// Lane i's page of key tile t: whether any row of the query tile may see it,
+// its pool row, and the granules it covers.
+struct PageLoad {
+  bool load;
+  int row;
+};
+
+__device__ __forceinline__ int pages_per_tile(const Geo& g) { return g.page_shift >= 7 ? 1 : BKV >> g.page_shift; }
+
+__device__ __forceinline__ PageLoad page_of_tile(const Geo& g, int b, const Span& u, int t, int i) {
+  PageLoad l{false, 0};
+  const int rows = g.page_shift >= 7 ? BKV : 1 << g.page_shift;
+  const int j = t * BKV + i * rows;  // first slot
+  const bool seen = (j < u.hi && j + rows > u.lo) || j < u.f;
+  if (!seen) return l;
+  const int page = __ldg(g.table + static_cast<long long>(b) * g.pages_per_seq + (j >> g.page_shift));
+  if (page < 0 || page >= g.num_pages) return l;
+  l.load = true;
+  l.row = (page << g.page_shift) + (j & ((1 << g.page_shift) - 1));
+  return l;
+}
+
+// Granule bits of the slots the tile's loads leave out, from the ballot of the
+// lanes that load.
+__device__ __forceinline__ uint32_t hole_bits(const Geo& g, uint32_t loaded) {
+  if (g.page_shift >= 7) return loaded & 1u ? 0u : 0xFFu;
+  const int per = (1 << g.page_shift) / GRANULE;  // granules per page: 1, 2 or 4
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < BKV / GRANULE; ++i)
+    if (!((loaded >> (i / per)) & 1u)) bits |= 1u << i;
+  return bits;
+}
+
+// Whether no row of the query tile sees slot j.
+__device__ __forceinline__ bool unseen(const Span& u, int j) { return !((j >= u.lo && j < u.hi) || j < u.f); }
+
+}  // namespace pg
+}  // namespace sea

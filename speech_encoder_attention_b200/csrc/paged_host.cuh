@@ -1,0 +1,288 @@
+// paged_host.cuh -- host side of the paged-cache entry points: argument
+// checks (pure arithmetic, before any CUDA call), launch plans and launches.
+// Included by attn_api.cu inside its unnamed namespace.
+
+constexpr int kMaxGroup = 32;  // query heads per K/V head
+
+bool misaligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) != 0; }
+
+Range byte_range(const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + static_cast<uintptr_t>(bytes)};
+}
+
+bool valid_paged_heads(int32_t batch, int32_t t_q, int32_t n_heads, int32_t n_kv_heads) {
+  if (batch <= 0 || batch > 65535 || t_q <= 0 || n_heads <= 0 || n_heads > 32767 || n_kv_heads <= 0) return false;
+  if (n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > kMaxGroup) return false;
+  return static_cast<int64_t>(batch) * t_q <= INT32_MAX && static_cast<int64_t>(t_q) * (n_heads / n_kv_heads) <= INT32_MAX / 2;
+}
+
+int64_t pool_rows(const attn_paged_kv& c) { return static_cast<int64_t>(c.num_pages) * c.page_size; }
+int64_t pool_cols(const attn_paged_kv& c) { return static_cast<int64_t>(c.n_kv_heads) * sea::pg::DH; }
+Range pool_range(const attn_paged_kv& c, const attn_mat& m) {
+  return mat_range(m.ptr, pool_rows(c), pool_cols(c), m.row_stride);
+}
+
+bool valid_cache(const attn_paged_kv& c, int32_t batch) {
+  if (c.page_size < 16 || c.page_size > 256 || (c.page_size & (c.page_size - 1)) != 0) return false;
+  if (c.num_pages <= 0 || c.pages_per_seq <= 0 || c.n_kv_heads <= 0 || c.n_kv_heads > 32767) return false;
+  if (pool_rows(c) > INT32_MAX) return false;
+  // slots per sequence stay below 2^23: a grid dimension counts their 128-slot tiles
+  if (static_cast<int64_t>(c.pages_per_seq) * c.page_size > (int64_t(1) << 23) - 256) return false;
+  if (static_cast<int64_t>(batch) * c.pages_per_seq * c.page_size > INT32_MAX) return false;
+  if (!valid_mat(c.k, pool_cols(c)) || !valid_mat(c.v, pool_cols(c))) return false;
+  return c.table != nullptr && !misaligned4(c.table) && c.kv_lens != nullptr && !misaligned4(c.kv_lens);
+}
+
+bool valid_paged_mask(const attn_paged_mask& m) {
+  return m.window >= 0 && m.first >= 0 && (m.window > 0 || m.first == 0) && (m.causal == 0 || m.causal == 1) &&
+         !misaligned4(m.q_lens);
+}
+
+int log2_of(int x) {
+  int l = 0;
+  while ((1 << l) < x) ++l;
+  return l;
+}
+
+sea::pg::Geo paged_geo(const attn_paged_kv& c, int32_t batch, int32_t t_q, int32_t n_heads, const attn_paged_mask& m) {
+  sea::pg::Geo g{};
+  g.batch = batch;
+  g.t_q = t_q;
+  g.n_heads = n_heads;
+  g.kv_heads = c.n_kv_heads;
+  g.group = n_heads / c.n_kv_heads;
+  g.tok_per_tile = 1;
+  g.q_tiles = t_q;
+  g.page_shift = log2_of(c.page_size);
+  g.pages_per_seq = c.pages_per_seq;
+  g.num_pages = c.num_pages;
+  g.cap = c.pages_per_seq * c.page_size;
+  g.table = c.table;
+  g.kv_lens = c.kv_lens;
+  g.q_lens = m.q_lens;
+  // |p - j| stays below t_q + cap: a wider window changes nothing, and the
+  // sums below stay in 32 bits.
+  const int64_t reach = static_cast<int64_t>(t_q) + g.cap + 1;
+  g.window = static_cast<int>(std::min<int64_t>(m.window, std::min<int64_t>(reach, INT32_MAX / 2)));
+  g.first = std::min(m.first, g.cap);
+  g.causal = m.causal;
+  return g;
+}
+
+bool encode_pages(CUtensorMap* m, const attn_paged_kv& c, const attn_mat& pool) {
+  const uint32_t box = static_cast<uint32_t>(std::min(c.page_size, sea::pg::BKV));
+  return encode_2d(m, pool.ptr, pool_cols(c), pool_rows(c), pool.row_stride * 2, sea::pg::DH, box,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+struct PagedPlan {
+  int rows_cap;       // rows of a query tile
+  int tok_per_tile, q_tiles;
+  int ctas;
+  size_t ws_bytes;
+};
+
+PagedPlan plan_paged(int t_q, int group, int num_sms) {
+  PagedPlan pl{};
+  pl.rows_cap = static_cast<int64_t>(t_q) * group <= 16 ? 16 : 32;
+  pl.tok_per_tile = std::max(1, std::min(t_q, pl.rows_cap / group));
+  pl.q_tiles = ceil_div(t_q, pl.tok_per_tile);
+  pl.ctas = 2 * num_sms;
+  pl.ws_bytes = size_t(2) * pl.ctas * pl.rows_cap * (sea::pg::DH * sizeof(float) + sizeof(float2));
+  return pl;
+}
+
+attn_status launch_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cache, int32_t batch, int32_t t_new,
+                                const int32_t* q_lens, cudaStream_t stream) {
+  if (!valid_paged_heads(batch, t_new, cache.n_kv_heads, cache.n_kv_heads) || !valid_cache(cache, batch))
+    return ATTN_ERR_INVALID;
+  if (misaligned4(q_lens)) return ATTN_ERR_INVALID;
+  const int64_t rows = static_cast<int64_t>(batch) * t_new, cols = pool_cols(cache);
+  if (!valid_mat(k_new, cols) || !valid_mat(v_new, cols)) return ATTN_ERR_INVALID;
+  for (const attn_mat& m : {k_new, v_new}) {
+    const Range r = mat_range(m.ptr, rows, cols, m.row_stride);
+    if (overlaps(r, pool_range(cache, cache.k)) || overlaps(r, pool_range(cache, cache.v))) return ATTN_ERR_INVALID;
+  }
+  DeviceInfo* dev = nullptr;
+  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  sea::pg::AppendParams p{};
+  attn_paged_mask none{};
+  none.q_lens = q_lens;
+  p.g = paged_geo(cache, batch, t_new, cache.n_kv_heads, none);
+  p.k_new = static_cast<const __half*>(k_new.ptr);
+  p.v_new = static_cast<const __half*>(v_new.ptr);
+  p.k_new_stride = k_new.row_stride;
+  p.v_new_stride = v_new.row_stride;
+  p.k = static_cast<__half*>(cache.k.ptr);
+  p.v = static_cast<__half*>(cache.v.ptr);
+  p.k_stride = cache.k.row_stride;
+  p.v_stride = cache.v.row_stride;
+  p.vecs = static_cast<int>(cols / 8);
+  const int64_t blocks = (rows * p.vecs + 255) / 256;
+  const int grid = static_cast<int>(std::min<int64_t>(blocks, int64_t(16) * dev->num_sms));
+  if (launch_pdl(sea::pg::paged_append_kernel, dim3(grid), dim3(256), 0, stream, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  return ATTN_OK;
+}
+
+attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                         attn_paged_mask mask, const float* sinks, float scale, attn_mat out, float* lse,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch) ||
+      !valid_paged_mask(mask))
+    return ATTN_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID;
+  const int64_t rows = static_cast<int64_t>(batch) * t_q, cols = static_cast<int64_t>(n_heads) * sea::pg::DH;
+  if (!valid_mat(q, cols) || !valid_mat(out, cols) || misaligned4(sinks) || misaligned4(lse)) return ATTN_ERR_INVALID;
+  const Range ro = mat_range(out.ptr, rows, cols, out.row_stride);
+  if (overlaps(ro, mat_range(q.ptr, rows, cols, q.row_stride)) || overlaps(ro, pool_range(cache, cache.k)) ||
+      overlaps(ro, pool_range(cache, cache.v)))
+    return ATTN_ERR_INVALID;
+  if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_INVALID;
+
+  DeviceInfo* dev = nullptr;
+  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  const PagedPlan pl = plan_paged(t_q, n_heads / cache.n_kv_heads, dev->num_sms);
+  if (workspace_bytes < pl.ws_bytes) return ATTN_ERR_INVALID;
+  const int64_t units = static_cast<int64_t>(batch) * cache.n_kv_heads * pl.q_tiles;
+  if (units > INT32_MAX) return ATTN_ERR_INVALID;
+
+  CUtensorMap tk, tv;
+  if (!encode_pages(&tk, cache, cache.k) || !encode_pages(&tv, cache, cache.v)) return ATTN_ERR_CUDA;
+  sea::pg::StepParams p{};
+  p.g = paged_geo(cache, batch, t_q, n_heads, mask);
+  p.g.tok_per_tile = pl.tok_per_tile;
+  p.g.q_tiles = pl.q_tiles;
+  p.q = static_cast<const __half*>(q.ptr);
+  p.q_stride = q.row_stride;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.sinks = sinks;
+  p.out = static_cast<__half*>(out.ptr);
+  p.out_stride = out.row_stride;
+  p.lse = lse;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + size_t(2) * pl.ctas * pl.rows_cap * sea::pg::DH);
+  p.rows_cap = pl.rows_cap;
+  p.least = 1;
+  p.err = dev->err;
+  p.limit_ns = sea::kDefaultTimeoutNs;
+  using sea::pg::StepCfg;
+  cudaError_t err = pl.rows_cap == 16
+                        ? launch_pdl(sea::pg::paged_step_kernel<1>, dim3(pl.ctas), dim3(StepCfg<1>::THREADS),
+                                     StepCfg<1>::SMEM_BYTES, stream, tk, tv, p)
+                        : launch_pdl(sea::pg::paged_step_kernel<2>, dim3(pl.ctas), dim3(StepCfg<2>::THREADS),
+                                     StepCfg<2>::SMEM_BYTES, stream, tk, tv, p);
+  if (err != cudaSuccess) return ATTN_ERR_CUDA;
+  const unsigned parts = static_cast<unsigned>(ceil_div(pl.rows_cap, 4 * sea::pg::COMBINE_WARPS));
+  if (launch_pdl(sea::pg::paged_combine_kernel, dim3(static_cast<unsigned>(units), parts),
+                 dim3(32 * sea::pg::COMBINE_WARPS), 0, stream, p, pl.ctas) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  return ATTN_OK;
+}
+
+attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                                 attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
+                                 cudaStream_t stream) {
+  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch) ||
+      !valid_paged_mask(mask))
+    return ATTN_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID;
+  const int64_t rows = static_cast<int64_t>(batch) * t_q, cols = static_cast<int64_t>(n_heads) * sea::pg::DH;
+  if (!valid_mat(q, cols) || lse == nullptr || misaligned4(lse) || w_out == nullptr || misaligned4(w_out) ||
+      misaligned4(w_in))
+    return ATTN_ERR_INVALID;
+  const Range rw = byte_range(w_out, 4 * static_cast<int64_t>(batch) * cache.pages_per_seq * cache.page_size);
+  if (w_in != nullptr && w_in != w_out && overlaps(rw, byte_range(w_in, static_cast<int64_t>(rw.hi - rw.lo))))
+    return ATTN_ERR_INVALID;
+  if (overlaps(rw, mat_range(q.ptr, rows, cols, q.row_stride)) || overlaps(rw, byte_range(lse, 4 * rows * n_heads)) ||
+      overlaps(rw, pool_range(cache, cache.k)))
+    return ATTN_ERR_INVALID;
+
+  DeviceInfo* dev = nullptr;
+  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  sea::pg::WeightParams p{};
+  p.g = paged_geo(cache, batch, t_q, n_heads, mask);
+  p.q = static_cast<const __half*>(q.ptr);
+  p.q_stride = q.row_stride;
+  p.k = static_cast<const __half*>(cache.k.ptr);
+  p.k_stride = cache.k.row_stride;
+  p.lse = lse;
+  p.w_in = w_in;
+  p.w_out = w_out;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.dv_group = make_divc(p.g.group);
+  const int tiles = ceil_div(p.g.cap, sea::pg::BKV);
+  const int64_t group_rows = static_cast<int64_t>(t_q) * p.g.group;
+  const bool few = group_rows <= 32;
+  // Ranks of a key tile's cluster: enough CTAs for about three per SM, as long
+  // as every rank has an item.
+  const int64_t items = few ? cache.n_kv_heads
+                            : static_cast<int64_t>(cache.n_kv_heads) * ceil_div(group_rows, sea::pg::WEIGHT_ROWS) / 2;
+  int ranks = 1;
+  while (ranks < 8 && 2 * ranks <= items && static_cast<int64_t>(tiles) * batch * ranks < 3 * dev->num_sms) ranks *= 2;
+  const dim3 grid(ranks, tiles, batch), block(32 * sea::pg::WEIGHT_WARPS);
+  const cudaError_t err =
+      few ? launch_pdl_cluster(sea::pg::paged_weights_kernel<1>, grid, block, 0, stream, ranks, p)
+          : launch_pdl_cluster(sea::pg::paged_weights_kernel<2>, grid, block, 0, stream, ranks, p);
+  return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,
+                               const float* w_in, attn_paged_kv dst, float* w_out, int32_t* kept, cudaStream_t stream) {
+  if (batch <= 0 || batch > 65535 || !valid_cache(cache, batch) || !valid_cache(dst, batch)) return ATTN_ERR_INVALID;
+  if (dst.page_size != cache.page_size || dst.n_kv_heads != cache.n_kv_heads) return ATTN_ERR_INVALID;
+  const int64_t cap = static_cast<int64_t>(cache.pages_per_seq) * cache.page_size;
+  const int64_t out_cap = static_cast<int64_t>(dst.pages_per_seq) * dst.page_size;
+  if (budget < 1 || budget > out_cap || first < 0 || recent < 0 || static_cast<int64_t>(first) + recent > budget)
+    return ATTN_ERR_INVALID;
+  if (w_in == nullptr || misaligned4(w_in) || misaligned4(w_out) || kept == nullptr || misaligned4(kept))
+    return ATTN_ERR_INVALID;
+  const Range r_win = byte_range(w_in, 4 * batch * cap), r_wout = byte_range(w_out, 4 * batch * out_cap);
+  const Range r_kept = byte_range(kept, 4 * static_cast<int64_t>(batch) * budget);
+  const Range r_lens = byte_range(dst.kv_lens, 4 * static_cast<int64_t>(batch));
+  if (w_out != nullptr && overlaps(r_win, r_wout) && !(w_out == w_in && cap == out_cap)) return ATTN_ERR_INVALID;
+  if (overlaps(r_kept, r_win) || (w_out != nullptr && (overlaps(r_kept, r_wout) || overlaps(r_lens, r_wout))) ||
+      overlaps(r_kept, r_lens) || overlaps(r_lens, r_win))
+    return ATTN_ERR_INVALID;
+  if (dst.kv_lens != cache.kv_lens && overlaps(r_lens, byte_range(cache.kv_lens, 4 * static_cast<int64_t>(batch))))
+    return ATTN_ERR_INVALID;
+  const bool same = cache.k.ptr == dst.k.ptr && cache.v.ptr == dst.v.ptr && cache.k.row_stride == dst.k.row_stride &&
+                    cache.v.row_stride == dst.v.row_stride && cache.num_pages == dst.num_pages;
+  if (!same)
+    for (const attn_mat& a : {cache.k, cache.v})
+      for (const attn_mat& b : {dst.k, dst.v})
+        if (overlaps(pool_range(cache, a), pool_range(dst, b))) return ATTN_ERR_INVALID;
+
+  DeviceInfo* dev = nullptr;
+  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  sea::pg::EvictParams p{};
+  p.g = paged_geo(cache, batch, 1, cache.n_kv_heads, attn_paged_mask{});
+  p.budget = budget;
+  p.first = first;
+  p.recent = recent;
+  p.w_in = w_in;
+  p.out_pages_per_seq = dst.pages_per_seq;
+  p.out_num_pages = dst.num_pages;
+  p.out_cap = static_cast<int>(out_cap);
+  p.out_table = dst.table;
+  p.out_lens = dst.kv_lens;
+  p.w_out = w_out;
+  p.kept = kept;
+  p.k = static_cast<const __half*>(cache.k.ptr);
+  p.v = static_cast<const __half*>(cache.v.ptr);
+  p.k_stride = cache.k.row_stride;
+  p.v_stride = cache.v.row_stride;
+  p.k_out = static_cast<__half*>(dst.k.ptr);
+  p.v_out = static_cast<__half*>(dst.v.ptr);
+  p.k_out_stride = dst.k.row_stride;
+  p.v_out_stride = dst.v.row_stride;
+  if (launch_pdl(sea::pg::paged_select_kernel, dim3(batch), dim3(sea::pg::SELECT_THREADS), 0, stream, p) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  // Other pools: rows in any order. The same pool: each CTA walks all rows upwards.
+  constexpr int kStep = sea::pg::MOVE_THREADS / 8 * sea::pg::MOVE_STEPS;
+  p.rows_per_cta = same ? budget : kStep;
+  const dim3 grid(ceil_div(budget, p.rows_per_cta), 2 * cache.n_kv_heads, batch);
+  if (launch_pdl(sea::pg::paged_move_kernel, grid, dim3(sea::pg::MOVE_THREADS), 0, stream, p) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  return ATTN_OK;
+}

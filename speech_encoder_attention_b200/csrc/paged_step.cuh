@@ -1,0 +1,487 @@
+// paged_step.cuh -- attention of a few new tokens over a paged K/V cache.
+//
+//   o_i = sum_{j in A_i} e^{s_ij} v_j / (sum_{j in A_i} e^{s_ij} [+ e^{sink_h}]),
+//   s_ij = scale <q_i, k_j>,  lse_i = ln of the denominator,
+// for query tiles of at most 16 * MT rows (the tokens of a chunk times the
+// query heads that share a K/V head). Bound by reading K and V once.
+//
+// A 128-row tcgen05 tile would leave at least 96 rows idle and costs a chain
+// of tensor-memory round trips per key tile; with so few rows each warp works
+// on its own instead: 16-row mma.sync products straight from shared memory,
+// P kept in registers, no step of one warp waiting for another inside a unit.
+//   warp 4      producer: one TMA copy per page into a ring of key tiles
+//               (128 slots of K and V, 128-byte swizzle); lane i reads the
+//               table entry of the tile's page i.
+//   warps 0-3   warp w takes slots [32w, 32w + 32) of every key tile with a
+//               running max, sum and output of its own; warp 0 merges the
+//               four at the end of a unit.
+// The key tiles of all units are cut into equal shares over two CTAs per SM;
+// units that are cut leave partials that paged_combine_kernel merges.
+#pragma once
+
+#include "paged_common.cuh"
+
+namespace sea {
+namespace pg {
+
+// The exponent reference of a row moves only when its max grows by more than
+// this (log2 units): p <= 2^15 fits fp16.
+constexpr float RESCALE_LIMIT = 15.0f;
+
+struct StepParams {
+  Geo g;
+  const __half* q;
+  int64_t q_stride;
+  float scale_log2;
+  const float* sinks;
+  __half* out;
+  int64_t out_stride;
+  float* lse;        // [batch * t_q, n_heads] or null
+  float* ws_o;       // [2 * CTAs][rows_cap][64] unnormalised partial O
+  float2* ws_ml;     // [2 * CTAs][rows_cap] (m in log2 units, l)
+  int rows_cap;
+  int least;         // fewest key tiles per CTA
+  uint32_t* err;
+  uint64_t limit_ns;
+};
+
+template <int MT>
+struct StepCfg {
+  static constexpr int ROWS = 16 * MT;
+  static constexpr int STAGES = MT == 1 ? 3 : 2;
+  static constexpr int WARPS = 4;
+  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = STAGES * TILE_BYTES;
+  static constexpr int MERGE_WARP = MT * (32 * 32 + 4 * 32);  // floats: O fragments, then m, l of two rows
+  static constexpr int OFF_MERGE = 2 * STAGES * TILE_BYTES;
+  static constexpr int OFF_BARS = OFF_MERGE + 3 * MERGE_WARP * 4;
+  static constexpr int NUM_BARS = 2 * STAGES + 2;  // full, empty, merge_full, merge_empty
+  static constexpr int OFF_HOLES = OFF_BARS + 8 * NUM_BARS;
+  static constexpr int OFF_MISC = OFF_HOLES + 4 * STAGES;
+  static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 8;
+};
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int MT>
+__global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
+    paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const StepParams p) {
+  using C = StepCfg<MT>;
+  constexpr int ST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BARS;
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (ST + s); };
+  const uint32_t merge_full = bar0 + 8u * (2 * ST), merge_empty = merge_full + 8u;
+  volatile uint32_t* holes = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_HOLES);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  const Geo& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), C::WARPS);
+    }
+    mbar_init(merge_full, C::WARPS - 1);
+    mbar_init(merge_empty, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  const WaitCtl wc{abort_flag, p.err, p.limit_ns};
+
+  Walk w;
+  const bool any = walk_start(g, w, blockIdx.x, gridDim.x, p.least);
+  if (any && warp == C::WARPS) {
+    // ---------------- producer ----------------
+    const int n_pages = pages_per_tile(g);
+    const uint32_t page_bytes = TILE_BYTES / n_pages;
+    int it = 0;
+    bool ok = true;
+    do {
+      for (int k = w.k0; k < w.k1 && ok; ++k, ++it) {
+        const int st = it % ST;
+        PageLoad l{false, 0};
+        if (lane < n_pages) l = page_of_tile(g, w.b, w.u, w.u.tile(k), lane);
+        const uint32_t loaded = __ballot_sync(0xffffffffu, l.load);
+        ok = mbar_wait(empty(st), ((it / ST) & 1) ^ 1u, wc);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          holes[st] = hole_bits(g, loaded);
+          mbar_arrive_expect_tx(full(st), 2u * __popc(loaded) * page_bytes);
+        }
+        __syncwarp();
+        if (l.load) {
+          tma_load_2d(sbase + C::OFF_K + st * TILE_BYTES + lane * page_bytes, &tm_k, full(st), w.h * DH, l.row);
+          tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, full(st), w.h * DH, l.row);
+        }
+      }
+    } while (ok && walk_next(g, w));
+    // Let the last copies land before the CTA may exit.
+    for (int i = max(0, it - ST); i < it; ++i) mbar_wait_drain(full(i % ST), (i / ST) & 1, p.limit_ns);
+  } else if (any) {
+    // ---------------- consumers ----------------
+    const int r4 = lane >> 2, c2 = (lane & 3) * 2;
+    const float sl2 = p.scale_log2;
+    float* merge_buf = reinterpret_cast<float*>(smem + C::OFF_MERGE);
+    int it = 0, unit = 0;
+    bool ok = true;
+    do {
+      const int rows = w.u.ntok * g.group;
+      // Q fragments straight from memory (2 KB per unit), and what each row sees.
+      uint32_t qf[MT][4][4];
+      RowSpan rs[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 16 * m + 8 * e + r4;
+          const bool valid = r < rows;
+          const int tok = w.u.tok0 + r / g.group;
+          const int head = w.h * g.group + r % g.group;
+          rs[m][e] = valid ? row_span(g, w.s, tok + w.s.off) : RowSpan{0, 0, 0};
+          const __half* src = p.q + (static_cast<int64_t>(w.b) * g.t_q + tok) * p.q_stride + head * DH + c2;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            qf[m][kk][e] = valid ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk)) : 0u;
+            qf[m][kk][2 + e] = valid ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8)) : 0u;
+          }
+        }
+      }
+      // Slots that every valid row sees need no mask.
+      const RowSpan r_first = row_span(g, w.s, w.u.tok0 + w.s.off);
+      const RowSpan r_last = row_span(g, w.s, w.u.tok0 + w.u.ntok - 1 + w.s.off);
+      const int all_lo = r_last.lo, all_hi = r_first.hi, all_f = r_first.f;
+      float o[MT][8][4];
+      float m_run[MT][2], l_run[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[m][d][e] = 0.f;
+        m_run[m][0] = m_run[m][1] = -INFINITY;
+        l_run[m][0] = l_run[m][1] = 0.f;
+      }
+      for (int k = w.k0; k < w.k1; ++k, ++it) {
+        const int st = it % ST;
+        if (!mbar_wait(full(st), (it / ST) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sk = sbase + C::OFF_K + st * TILE_BYTES + warp * 32 * 128;
+        const uint32_t sv = sbase + C::OFF_V + st * TILE_BYTES + warp * 32 * 128;
+        const int j0 = w.u.tile(k) * BKV + warp * 32;  // this warp's first slot
+        const uint32_t hole = (holes[st] >> (2 * warp)) & 3u;
+        // S = Q K^T, 32 slots in four groups of 8
+        float s[MT][4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t b[2][4];
+          const int row = 8 * n + (lane & 7);
+          const int ch = lane >> 3;
+          ldmatrix_x4(sk + row * 128 + ((ch ^ (row & 7)) << 4), b[0]);
+          ldmatrix_x4(sk + row * 128 + (((ch + 4) ^ (row & 7)) << 4), b[1]);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[m][n][e] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_16816(s[m][n], qf[m][kk], b[kk >> 1][2 * (kk & 1)], b[kk >> 1][2 * (kk & 1) + 1]);
+          }
+        }
+        const bool edge = hole != 0 || !((j0 >= all_lo && j0 + 32 <= all_hi) || j0 + 32 <= all_f);
+        // Values of slots no row sees (behind the end, outside the window, in
+        // a page that was not loaded) may be anything: they are cleared.
+        uint32_t keep[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int j = j0 + 8 * n + c2 + x;
+              const bool gone = (hole >> (n >> 1)) & 1u;
+              if (gone || unseen(w.u, j)) keep[n >> 1][n & 1] &= x ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const RowSpan& r = rs[m][e];
+                  if (gone || !((j >= r.lo && j < r.hi) || j < r.f)) s[m][n][2 * e + x] = -INFINITY;
+                }
+            }
+          }
+        }
+        uint32_t pf[MT][2][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) mx = fmax3(mx, s[m][n][2 * e], s[m][n][2 * e + 1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mx2 = mx * sl2;
+            const bool grow = mx2 > m_run[m][e] + RESCALE_LIMIT;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float m_new = grow ? mx2 : m_run[m][e];
+              const float alpha = grow ? ex2_approx(m_run[m][e] - m_new) : 1.f;
+              l_run[m][e] *= alpha;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                o[m][d][2 * e] *= alpha;
+                o[m][d][2 * e + 1] *= alpha;
+              }
+              m_run[m][e] = m_new;
+            }
+            const float ref = m_run[m][e] == -INFINITY ? 0.f : m_run[m][e];
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const float p0 = ex2_approx(fmaf(s[m][n][2 * e], sl2, -ref));
+              const float p1 = ex2_approx(fmaf(s[m][n][2 * e + 1], sl2, -ref));
+              sum += p0 + p1;
+              // P is rounded to fp16 for the tensor cores; the sum is not
+              pf[m][n >> 1][(n & 1) * 2 + e] = pack_half2(p0, p1);
+            }
+            l_run[m][e] += sum;
+          }
+        }
+        // O += P V
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+          for (int dp = 0; dp < 4; ++dp) {
+            uint32_t b[4];
+            const int row = 16 * kk + (lane & 15);
+            const int ch = 2 * dp + (lane >> 4);
+            ldmatrix_x4_trans(sv + row * 128 + ((ch ^ (row & 7)) << 4), b);
+            if (edge) {
+              b[0] &= keep[kk][0];
+              b[1] &= keep[kk][1];
+              b[2] &= keep[kk][0];
+              b[3] &= keep[kk][1];
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_16816(o[m][2 * dp], pf[m][kk], b[0], b[1]);
+              mma_16816(o[m][2 * dp + 1], pf[m][kk], b[2], b[3]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(st));
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l_run[m][e] += __shfl_xor_sync(0xffffffffu, l_run[m][e], 1);
+          l_run[m][e] += __shfl_xor_sync(0xffffffffu, l_run[m][e], 2);
+        }
+      // Warps 1-3 hand their partials to warp 0 in fragment order.
+      if (warp != 0) {
+        if (unit > 0 && !mbar_wait(merge_empty, (unit - 1) & 1, wc)) break;
+        float* dst = merge_buf + (warp - 1) * C::MERGE_WARP;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) dst[(m * 32 + i) * 32 + lane] = o[m][i >> 2][i & 3];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            dst[MT * 1024 + (m * 4 + e) * 32 + lane] = m_run[m][e];
+            dst[MT * 1024 + (m * 4 + 2 + e) * 32 + lane] = l_run[m][e];
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merge_full);
+      } else {
+        if (!mbar_wait(merge_full, unit & 1, wc)) break;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mw[3], lw[3];
+            float mx = l_run[m][e] > 0.f ? m_run[m][e] : -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              const float* src = merge_buf + i * C::MERGE_WARP + MT * 1024;
+              mw[i] = src[(m * 4 + e) * 32 + lane];
+              lw[i] = src[(m * 4 + 2 + e) * 32 + lane];
+              if (lw[i] > 0.f) mx = fmaxf(mx, mw[i]);
+            }
+            const float own = l_run[m][e] > 0.f ? ex2_approx(m_run[m][e] - mx) : 0.f;
+            float l = l_run[m][e] * own;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              o[m][d][2 * e] = own > 0.f ? o[m][d][2 * e] * own : 0.f;
+              o[m][d][2 * e + 1] = own > 0.f ? o[m][d][2 * e + 1] * own : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              if (lw[i] > 0.f) {
+                const float wgt = ex2_approx(mw[i] - mx);
+                l += lw[i] * wgt;
+                const float* src = merge_buf + i * C::MERGE_WARP + m * 1024;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                  o[m][d][2 * e] += src[(d * 4 + 2 * e) * 32 + lane] * wgt;
+                  o[m][d][2 * e + 1] += src[(d * 4 + 2 * e + 1) * 32 + lane] * wgt;
+                }
+              }
+            }
+            const int r = 16 * m + 8 * e + r4;
+            if (r < rows) {
+              if (w.whole) {
+                const int64_t row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + r / g.group;
+                const int head = w.h * g.group + r % g.group;
+                if (p.sinks != nullptr && l > 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                __half* dst = p.out + row * p.out_stride + head * DH + c2;
+#pragma unroll
+                for (int d = 0; d < 8; ++d)
+                  *reinterpret_cast<uint32_t*>(dst + 8 * d) =
+                      l > 0.f ? pack_half2(o[m][d][2 * e] * inv, o[m][d][2 * e + 1] * inv) : 0u;
+                if (p.lse != nullptr && c2 == 0)
+                  p.lse[row * g.n_heads + head] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+              } else {
+                const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + w.slot) * p.rows_cap + r;
+                float2* dst = reinterpret_cast<float2*>(p.ws_o + part * DH + c2);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) dst[4 * d] = make_float2(o[m][d][2 * e], o[m][d][2 * e + 1]);
+                if (c2 == 0) p.ws_ml[part] = make_float2(mx, l);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merge_empty);
+      }
+      ++unit;
+    } while (walk_next(g, w));
+  }
+  __syncthreads();
+}
+
+// Merges the partials of cut units and writes the rows that no share holds:
+// one warp per row (token, query head) of a unit, block (unit, group of rows).
+//   M = max_s m_s,  L = sum_s l_s 2^(m_s - M) [+ 2^(sink log2e - M)],
+//   o = sum_s O_s 2^(m_s - M) / L.
+// Rows without a visible slot, and padding rows, are zero with lse = -inf.
+// Bound by its latency: the partials lie in L2.
+constexpr int COMBINE_WARPS = 8;
+
+__global__ void __launch_bounds__(32 * COMBINE_WARPS, 4)
+    paged_combine_kernel(const StepParams p, int ctas) {
+  const Geo& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int unit = blockIdx.x;
+  const int qt = unit % g.q_tiles;
+  const int h = unit / g.q_tiles % g.kv_heads;
+  const int b = unit / g.q_tiles / g.kv_heads;
+  const Seq s = seq_of(g, b);
+  const Span u = span_of(g, s, qt);
+  const int rows_out = min(g.tok_per_tile, g.t_q - u.tok0) * g.group;  // valid and padding rows
+  const int rows = u.ntok * g.group;
+  long long u0 = 0, per = 1;
+  bool cut = false;
+  if (u.n > 0) {
+    per = share_of(tiles_before(g, g.batch), ctas, p.least);
+    u0 = tiles_before(g, b) + static_cast<long long>(h) * tiles_before_q(g, s, g.q_tiles) + tiles_before_q(g, s, qt);
+    cut = u0 / per != (u0 + u.n - 1) / per;
+  }
+  const int c0 = static_cast<int>(u0 / per), c1 = u.n > 0 ? static_cast<int>((u0 + u.n - 1) / per) : 0;
+  const bool c0_first = u0 == per * c0;
+  for (int r = blockIdx.y * COMBINE_WARPS + warp; r < rows_out; r += gridDim.y * COMBINE_WARPS) {
+    const int64_t row = static_cast<int64_t>(b) * g.t_q + u.tok0 + r / g.group;
+    const int head = h * g.group + r % g.group;
+    const bool filled = r < rows && u.n > 0;
+    if (filled && !cut) continue;  // written by the share that holds the unit
+    float l = 0.f, o0 = 0.f, o1 = 0.f, mmax = -INFINITY;
+    if (filled) {
+      const int parts = c1 - c0 + 1;
+      auto slot_of = [&](int i) -> int64_t {
+        const int64_t c = c0 + i;
+        return (2 * c + (i == 0 && !c0_first ? 1 : 0)) * p.rows_cap + r;
+      };
+      for (int i0 = 0; i0 < parts; i0 += 32) {
+        float m = -INFINITY;
+        if (i0 + lane < parts) {
+          const float2 ml = p.ws_ml[slot_of(i0 + lane)];
+          if (ml.y > 0.f) m = ml.x;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        mmax = fmaxf(mmax, m);
+      }
+      if (mmax != -INFINITY) {
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+          float wgt = 0.f, lw = 0.f;
+          if (i0 + lane < parts) {
+            const float2 ml = p.ws_ml[slot_of(i0 + lane)];
+            if (ml.y > 0.f) {
+              wgt = ex2_approx(ml.x - mmax);
+              lw = ml.y * wgt;
+            }
+          }
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+          l += lw;
+          const int n = min(32, parts - i0);
+#pragma unroll 4
+          for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, wgt, i);
+            const float2 v = *(reinterpret_cast<const float2*>(p.ws_o + slot_of(i0 + i) * DH) + lane);
+            if (wi > 0.f) {
+              o0 += v.x * wi;
+              o1 += v.y * wi;
+            }
+          }
+        }
+        if (p.sinks != nullptr) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mmax);
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    *(reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + head * DH) + lane) =
+        l > 0.f ? pack_half2(o0 * inv, o1 * inv) : 0u;
+    if (p.lse != nullptr && lane == 0) p.lse[row * g.n_heads + head] = l > 0.f ? mmax * kLn2 + logf(l) : -INFINITY;
+  }
+}
+
+}  // namespace pg
+}  // namespace sea
