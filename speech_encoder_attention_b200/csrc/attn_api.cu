@@ -689,7 +689,7 @@ size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, in
   if (!valid_paged_heads(batch, t_q, n_heads, n_kv_heads)) return 0;
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != ATTN_OK) return 0;
-  return plan_paged(t_q, n_heads / n_kv_heads, dev->num_sms).ws_bytes;
+  return plan_paged(t_q, n_heads, n_kv_heads, dev->num_sms).ws_bytes;
 }
 
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,

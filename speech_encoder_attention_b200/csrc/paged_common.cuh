@@ -99,9 +99,11 @@ __device__ __forceinline__ Span span_of(const Geo& g, const Seq& s, int qt) {
 }
 
 // ---------------------------------------------------------------------------
-// work split: the key tiles of all (sequence, K/V head, query tile) units in
-// one line, cut into equal shares, one per CTA. A unit whose tiles fall into
-// several shares leaves unnormalised partials in the workspace.
+// work split: the key tiles of all (sequence, query tile) units in one line,
+// cut into equal parts; CTA part * kv_heads + h walks its part for K/V head h.
+// The heads of a part run side by side over the same slots, whose rows lie next
+// to each other in memory. A unit whose tiles fall into several parts leaves
+// unnormalised partials in the workspace.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ int tiles_of_seq(const Geo& g, int b) {
@@ -111,9 +113,8 @@ __device__ __forceinline__ int tiles_of_seq(const Geo& g, int b) {
   return n;
 }
 
-// One warp: the tiles of all sequences before b (times K/V heads) and, with
-// b == batch, of all. Lanes take sequences; with many query tiles per
-// sequence they take query tiles.
+// One warp: the tiles of all sequences before b (b == batch: of all). Lanes
+// take sequences; with many query tiles per sequence they take query tiles.
 __device__ __forceinline__ long long tiles_before(const Geo& g, int b) {
   const int lane = threadIdx.x & 31;
   long long sum = 0;
@@ -127,7 +128,7 @@ __device__ __forceinline__ long long tiles_before(const Geo& g, int b) {
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * g.kv_heads;
+  return sum;
 }
 
 // Tiles of query tiles [0, qt) of one sequence (one warp).
@@ -139,22 +140,22 @@ __device__ __forceinline__ int tiles_before_q(const Geo& g, const Seq& s, int qt
   return sum;
 }
 
-// Tiles per CTA: an equal share, at least `least`.
-__device__ __forceinline__ long long share_of(long long total, int ctas, int least) {
-  const long long per = (total + ctas - 1) / ctas;
+// Tiles per part: an equal share, at least `least`.
+__device__ __forceinline__ long long share_of(long long total, int parts, int least) {
+  const long long per = (total + parts - 1) / parts;
   return per < least ? least : per;
 }
 
-// One CTA's share, unit by unit. Every warp of the CTA walks the same steps.
+// One part, unit by unit. Every warp of the CTA walks the same steps.
 struct Walk {
   long long pos, end;   // tiles left: [pos, end)
   long long begin;
-  int b, h, qt;
+  int b, qt;
   Seq s;
   Span u;
   int k0, k1;           // key tiles [k0, k1) of the unit u
   bool whole;           // the unit's tiles are all here
-  int slot;             // partial slot of this share (0: its first unit, 1: a later one)
+  int slot;             // partial slot of this part (0: its first unit, 1: a later one)
 };
 
 __device__ __forceinline__ void walk_cut(const Geo& g, Walk& w, int k0) {
@@ -165,21 +166,21 @@ __device__ __forceinline__ void walk_cut(const Geo& g, Walk& w, int k0) {
   w.slot = w.pos == w.begin ? 0 : 1;
 }
 
-// One warp; returns false if the share is empty.
-__device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int cta, int ctas, int least) {
+// One warp; returns false if the part is empty.
+__device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int part, int parts, int least) {
   const int lane = threadIdx.x & 31;
   const long long total = tiles_before(g, g.batch);
-  const long long per = share_of(total, ctas, least);
-  w.begin = w.pos = per * cta;
+  const long long per = share_of(total, parts, least);
+  w.begin = w.pos = per * part;
   w.end = min(total, w.pos + per);
   if (w.pos >= w.end) return false;
   // the sequence that holds tile `pos`
   long long base = 0;
-  int b = 0, seq_tiles = 0;
+  int b = 0;
   if (g.q_tiles <= 4) {
     for (int b0 = 0; b0 < g.batch; b0 += 32) {
       const int n = b0 + lane < g.batch ? tiles_of_seq(g, b0 + lane) : 0;
-      long long incl = static_cast<long long>(n) * g.kv_heads;
+      long long incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long t = __shfl_up_sync(0xffffffffu, incl, o);
@@ -189,25 +190,21 @@ __device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int cta, int c
       if (past) {
         const int i = __ffs(past) - 1;
         b = b0 + i;
-        seq_tiles = __shfl_sync(0xffffffffu, n, i);
-        base += __shfl_sync(0xffffffffu, incl, i) - static_cast<long long>(seq_tiles) * g.kv_heads;
+        base += __shfl_sync(0xffffffffu, incl - n, i);
         break;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
   } else {
     for (b = 0; b < g.batch; ++b) {
-      seq_tiles = tiles_before_q(g, seq_of(g, b), g.q_tiles);
-      const long long n = static_cast<long long>(seq_tiles) * g.kv_heads;
+      const int n = tiles_before_q(g, seq_of(g, b), g.q_tiles);
       if (base + n > w.pos) break;
       base += n;
     }
   }
-  const long long in_seq = w.pos - base;
   w.b = b;
   w.s = seq_of(g, b);
-  w.h = static_cast<int>(in_seq / seq_tiles);
-  int rest = static_cast<int>(in_seq - static_cast<long long>(w.h) * seq_tiles);
+  int rest = static_cast<int>(w.pos - base);
   // the query tile that holds it
   int qt = 0;
   for (int q0 = 0; q0 < g.q_tiles; q0 += 32) {
@@ -233,18 +230,15 @@ __device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int cta, int c
   return true;
 }
 
-// The next unit of the share; false when the share is done. Any thread.
+// The next unit of the part; false when the part is done. Any thread.
 __device__ __forceinline__ bool walk_next(const Geo& g, Walk& w) {
   w.pos += w.k1 - w.k0;
   if (w.pos >= w.end) return false;
   do {
     if (++w.qt == g.q_tiles) {
       w.qt = 0;
-      if (++w.h == g.kv_heads) {
-        w.h = 0;
-        ++w.b;
-        w.s = seq_of(g, w.b);
-      }
+      ++w.b;
+      w.s = seq_of(g, w.b);
     }
     w.u = span_of(g, w.s, w.qt);
   } while (w.u.n == 0);

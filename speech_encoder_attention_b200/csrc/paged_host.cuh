@@ -70,25 +70,37 @@ sea::pg::Geo paged_geo(const attn_paged_kv& c, int32_t batch, int32_t t_q, int32
   return g;
 }
 
+// One K/V head's 128 bytes of up to 128 pool rows. L2 fetches 128 bytes per
+// row, not 256: the next head's half belongs to another CTA, which comes for it
+// at another time (16 decode steps over 8k caches: 108 us with 256 bytes, which
+// read a third more from memory).
 bool encode_pages(CUtensorMap* m, const attn_paged_kv& c, const attn_mat& pool) {
-  const uint32_t box = static_cast<uint32_t>(std::min(c.page_size, sea::pg::BKV));
-  return encode_2d(m, pool.ptr, pool_cols(c), pool_rows(c), pool.row_stride * 2, sea::pg::DH, box,
-                   CU_TENSOR_MAP_SWIZZLE_128B);
+  auto enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(pool_cols(c)), static_cast<cuuint64_t>(pool_rows(c))};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pool.row_stride) * 2};
+  cuuint32_t box[2] = {sea::pg::DH, static_cast<cuuint32_t>(std::min(c.page_size, sea::pg::BKV))};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, pool.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
   int tok_per_tile, q_tiles;
-  int ctas;
+  int parts, ctas;    // CTAs: one per part and K/V head
   size_t ws_bytes;
 };
 
-PagedPlan plan_paged(int t_q, int group, int num_sms) {
+PagedPlan plan_paged(int t_q, int n_heads, int kv_heads, int num_sms) {
+  const int group = n_heads / kv_heads;
   PagedPlan pl{};
   pl.rows_cap = static_cast<int64_t>(t_q) * group <= 16 ? 16 : 32;
   pl.tok_per_tile = std::max(1, std::min(t_q, pl.rows_cap / group));
   pl.q_tiles = ceil_div(t_q, pl.tok_per_tile);
-  pl.ctas = 2 * num_sms;
+  pl.parts = std::max(1, 2 * num_sms / kv_heads);
+  pl.ctas = pl.parts * kv_heads;
   pl.ws_bytes = size_t(2) * pl.ctas * pl.rows_cap * (sea::pg::DH * sizeof(float) + sizeof(float2));
   return pl;
 }
@@ -142,7 +154,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
 
   DeviceInfo* dev = nullptr;
   if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
-  const PagedPlan pl = plan_paged(t_q, n_heads / cache.n_kv_heads, dev->num_sms);
+  const PagedPlan pl = plan_paged(t_q, n_heads, cache.n_kv_heads, dev->num_sms);
   if (workspace_bytes < pl.ws_bytes) return ATTN_ERR_INVALID;
   const int64_t units = static_cast<int64_t>(batch) * cache.n_kv_heads * pl.q_tiles;
   if (units > INT32_MAX) return ATTN_ERR_INVALID;
@@ -163,6 +175,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + size_t(2) * pl.ctas * pl.rows_cap * sea::pg::DH);
   p.rows_cap = pl.rows_cap;
+  p.parts = pl.parts;
   p.least = 1;
   p.err = dev->err;
   p.limit_ns = sea::kDefaultTimeoutNs;
@@ -175,7 +188,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
   const unsigned parts = static_cast<unsigned>(ceil_div(pl.rows_cap, 4 * sea::pg::COMBINE_WARPS));
   if (launch_pdl(sea::pg::paged_combine_kernel, dim3(static_cast<unsigned>(units), parts),
-                 dim3(32 * sea::pg::COMBINE_WARPS), 0, stream, p, pl.ctas) != cudaSuccess)
+                 dim3(32 * sea::pg::COMBINE_WARPS), 0, stream, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }

@@ -15,8 +15,9 @@
 //   warps 0-3   warp w takes slots [32w, 32w + 32) of every key tile with a
 //               running max, sum and output of its own; warp 0 merges the
 //               four at the end of a unit.
-// The key tiles of all units are cut into equal shares over two CTAs per SM;
-// units that are cut leave partials that paged_combine_kernel merges.
+// The key tiles of all units are cut into equal parts, a CTA for each part and
+// K/V head, two CTAs per SM; units that are cut leave partials that
+// paged_combine_kernel merges.
 #pragma once
 
 #include "paged_common.cuh"
@@ -40,7 +41,8 @@ struct StepParams {
   float* ws_o;       // [2 * CTAs][rows_cap][64] unnormalised partial O
   float2* ws_ml;     // [2 * CTAs][rows_cap] (m in log2 units, l)
   int rows_cap;
-  int least;         // fewest key tiles per CTA
+  int parts;         // the line of key tiles is cut into this many
+  int least;         // fewest key tiles per part
   uint32_t* err;
   uint64_t limit_ns;
 };
@@ -119,8 +121,9 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
   griddep_launch_dependents();
   const WaitCtl wc{abort_flag, p.err, p.limit_ns};
 
+  const int h = blockIdx.x % g.kv_heads;
   Walk w;
-  const bool any = walk_start(g, w, blockIdx.x, gridDim.x, p.least);
+  const bool any = walk_start(g, w, blockIdx.x / g.kv_heads, p.parts, p.least);
   if (any && warp == C::WARPS) {
     // ---------------- producer ----------------
     const int n_pages = pages_per_tile(g);
@@ -142,8 +145,8 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
         }
         __syncwarp();
         if (l.load) {
-          tma_load_2d(sbase + C::OFF_K + st * TILE_BYTES + lane * page_bytes, &tm_k, full(st), w.h * DH, l.row);
-          tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, full(st), w.h * DH, l.row);
+          tma_load_2d(sbase + C::OFF_K + st * TILE_BYTES + lane * page_bytes, &tm_k, full(st), h * DH, l.row);
+          tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, full(st), h * DH, l.row);
         }
       }
     } while (ok && walk_next(g, w));
@@ -168,7 +171,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
           const int r = 16 * m + 8 * e + r4;
           const bool valid = r < rows;
           const int tok = w.u.tok0 + r / g.group;
-          const int head = w.h * g.group + r % g.group;
+          const int head = h * g.group + r % g.group;
           rs[m][e] = valid ? row_span(g, w.s, tok + w.s.off) : RowSpan{0, 0, 0};
           const __half* src = p.q + (static_cast<int64_t>(w.b) * g.t_q + tok) * p.q_stride + head * DH + c2;
 #pragma unroll
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
             if (r < rows) {
               if (w.whole) {
                 const int64_t row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + r / g.group;
-                const int head = w.h * g.group + r % g.group;
+                const int head = h * g.group + r % g.group;
                 if (p.sinks != nullptr && l > 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __half* dst = p.out + row * p.out_stride + head * DH + c2;
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
   __syncthreads();
 }
 
-// Merges the partials of cut units and writes the rows that no share holds:
+// Merges the partials of cut units and writes the rows that no CTA holds:
 // one warp per row (token, query head) of a unit, block (unit, group of rows).
 //   M = max_s m_s,  L = sum_s l_s 2^(m_s - M) [+ 2^(sink log2e - M)],
 //   o = sum_s O_s 2^(m_s - M) / L.
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
 constexpr int COMBINE_WARPS = 8;
 
 __global__ void __launch_bounds__(32 * COMBINE_WARPS, 4)
-    paged_combine_kernel(const StepParams p, int ctas) {
+    paged_combine_kernel(const StepParams p) {
   const Geo& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
@@ -421,8 +424,8 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 4)
   long long u0 = 0, per = 1;
   bool cut = false;
   if (u.n > 0) {
-    per = share_of(tiles_before(g, g.batch), ctas, p.least);
-    u0 = tiles_before(g, b) + static_cast<long long>(h) * tiles_before_q(g, s, g.q_tiles) + tiles_before_q(g, s, qt);
+    per = share_of(tiles_before(g, g.batch), p.parts, p.least);
+    u0 = tiles_before(g, b) + tiles_before_q(g, s, qt);
     cut = u0 / per != (u0 + u.n - 1) / per;
   }
   const int c0 = static_cast<int>(u0 / per), c1 = u.n > 0 ? static_cast<int>((u0 + u.n - 1) / per) : 0;
@@ -431,12 +434,12 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 4)
     const int64_t row = static_cast<int64_t>(b) * g.t_q + u.tok0 + r / g.group;
     const int head = h * g.group + r % g.group;
     const bool filled = r < rows && u.n > 0;
-    if (filled && !cut) continue;  // written by the share that holds the unit
+    if (filled && !cut) continue;  // written by the CTA that holds the unit
     float l = 0.f, o0 = 0.f, o1 = 0.f, mmax = -INFINITY;
     if (filled) {
       const int parts = c1 - c0 + 1;
       auto slot_of = [&](int i) -> int64_t {
-        const int64_t c = c0 + i;
+        const int64_t c = static_cast<int64_t>(c0 + i) * g.kv_heads + h;
         return (2 * c + (i == 0 && !c0_first ? 1 : 0)) * p.rows_cap + r;
       };
       for (int i0 = 0; i0 < parts; i0 += 32) {
