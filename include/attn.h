@@ -312,7 +312,7 @@ attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cach
  *   o_i = sum_{j in A_i} e^{s_ij} v_j / D_i,  D_i = sum_{j in A_i} e^{s_ij} [+ e^{sinks[h]}],
  *   s_ij = scale * <q_i, k_j>,  lse_i = ln D_i              per query head h
  * Query head h reads K/V head h / (n_heads / n_kv_heads); n_heads must be a
- * multiple of n_kv_heads, with at most 32 query heads per K/V head.
+ * multiple of n_kv_heads, with at most 128 query heads per K/V head.
  *   q, out   [batch*t_q, n_heads*64] fp16; out must not overlap q or the pools
  *   sinks    [n_heads] fp32 or NULL, as in attn_forward_sinks
  *   lse      [batch*t_q, n_heads] fp32 or NULL

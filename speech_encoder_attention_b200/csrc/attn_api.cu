@@ -17,6 +17,7 @@
 #include "attn.h"
 #include "flash_attn.cuh"
 #include "paged_cache.cuh"
+#include "paged_chunk.cuh"
 #include "paged_common.cuh"
 #include "paged_step.cuh"
 #include "paged_weights.cuh"
@@ -135,6 +136,8 @@ attn_status device_info(DeviceInfo** out) {
                              sea::pg::StepCfg<1>::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::pg::paged_step_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::pg::StepCfg<2>::SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(sea::pg::paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sea::pg::ChunkCfg::SMEM_BYTES) != cudaSuccess ||
         !set_attention_smem<2>() || !set_attention_smem<4>())
       return ATTN_ERR_CUDA;
     d.num_sms = sms;

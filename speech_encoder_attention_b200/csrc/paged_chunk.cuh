@@ -1,0 +1,444 @@
+// paged_chunk.cuh -- attention of a chunk of new tokens over a paged K/V cache
+// on Blackwell tensor cores (the definitions are in paged_step.cuh).
+//
+// For query tiles of more than 32 rows (a row is a token and one of the query
+// heads that share a K/V head; up to 128 rows). Bound by the exponentials, one
+// per (row, slot), as flash_attn_kernel is, whose roles and tensor-memory
+// layout this kernel shares: 192 threads, two CTAs per SM.
+//   warps 0-3  softmax, one thread per row; they also clear the values of slots
+//              that no row of the tile sees and write the output.
+//   warp 4     TMA producer: Q through a 4-D map (column, head, token,
+//              sequence), K and V one copy per page.
+//   warp 5     tcgen05.mma issuer: S = Q K^T, then O += P V.
+// Two ways to deal out the work. With many units (sequence, head, query tile)
+// each CTA walks whole units, the ones at the end of the prompts, which see
+// most, first. With few, the key tiles of all units are cut into equal parts as
+// in paged_step_kernel, and paged_combine_kernel merges what was cut.
+#pragma once
+
+#include "flash_attn.cuh"
+#include "paged_common.cuh"
+#include "paged_step.cuh"
+
+namespace sea {
+namespace pg {
+
+struct ChunkCfg : fa::CfgT<2> {
+  static constexpr int OFF_HOLES = OFF_MISC + 8;
+  static constexpr int SMEM_BYTES = 1024 + OFF_HOLES + 4 * STAGES;
+};
+
+struct ChunkParams {
+  StepParams s;
+  int cut;             // 1: equal parts, 0: whole units
+  int units;           // batch * kv_heads * q_tiles
+  fa::DivC dv_group, dv_heads, dv_bh;  // by group, kv_heads, batch * kv_heads
+};
+
+// The units of a CTA: a Walk over its part, or units blockIdx.x, + gridDim.x, ...
+// with the last query tiles of all sequences and heads first.
+struct ChunkWalk : Walk {
+  int h, unit;
+};
+
+__device__ __forceinline__ void chunk_unit(const ChunkParams& p, ChunkWalk& w) {
+  const Geo& g = p.s.g;
+  const int back = fa::div_c(w.unit, p.dv_bh);
+  const int bh = w.unit - back * (g.batch * g.kv_heads);
+  w.qt = g.q_tiles - 1 - back;
+  w.b = fa::div_c(bh, p.dv_heads);
+  w.h = bh - w.b * g.kv_heads;
+  w.s = seq_of(g, w.b);
+  w.u = span_of(g, w.s, w.qt);
+  w.k0 = 0;
+  w.k1 = w.u.n;
+  w.whole = true;
+}
+
+// One warp.
+__device__ __forceinline__ bool chunk_start(const ChunkParams& p, ChunkWalk& w) {
+  const Geo& g = p.s.g;
+  if (p.cut) {
+    w.h = blockIdx.x % g.kv_heads;
+    return walk_start(g, w, blockIdx.x / g.kv_heads, p.s.parts, p.s.least);
+  }
+  w.unit = blockIdx.x;
+  if (w.unit >= p.units) return false;
+  chunk_unit(p, w);
+  return true;
+}
+
+__device__ __forceinline__ bool chunk_next(const ChunkParams& p, ChunkWalk& w) {
+  if (p.cut) return walk_next(p.s.g, w);
+  w.unit += gridDim.x;
+  if (w.unit >= p.units) return false;
+  chunk_unit(p, w);
+  return true;
+}
+
+__global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const ChunkParams cp) {
+  using C = ChunkCfg;
+  constexpr int ST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + C::OFF_BARS;
+  auto q_full = [&](int i) { return bar0 + 8u * i; };
+  auto q_empty = [&](int i) { return bar0 + 8u * (2 + i); };
+  auto k_full = [&](int s) { return bar0 + 8u * (4 + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (4 + ST + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + 2 * ST + s); };
+  const uint32_t s_full = bar0 + 8u * (4 + 3 * ST);
+  const uint32_t s_free = s_full + 8u;
+  const uint32_t p_full = s_full + 16u;
+  const uint32_t o_done = s_full + 24u;
+  const uint32_t o_free = s_full + 32u;
+  const uint32_t drain_bar = s_full + 40u;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
+  volatile uint32_t* holes = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_HOLES);
+  const StepParams& p = cp.s;
+  const Geo& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full(i), 1);
+      mbar_init(q_empty(i), 1);
+    }
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(v_full(s), 1);
+      mbar_init(kv_empty(s), 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
+    mbar_init(o_done, 1);
+    mbar_init(o_free, 4);
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0u;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+  const WaitCtl wc{abort_flag, p.err, p.limit_ns};
+
+  ChunkWalk w;
+  const bool any = chunk_start(cp, w);
+  if (any && warp == C::PRODUCER_WARP) {
+    // ---------------- TMA producer (whole warp: lane i loads page i of a tile) ----------------
+    const int n_pages = pages_per_tile(g);
+    const uint32_t page_bytes = TILE_BYTES / n_pages;
+    const uint32_t q_bytes = static_cast<uint32_t>(g.tok_per_tile * g.group) * DH * 2;
+    int qn = 0, it = 0;
+    bool ok = true;
+    do {
+      if (w.k1 <= w.k0) continue;
+      const int qb = qn & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(q_empty(qb), ((qn >> 1) & 1) ^ 1u, wc));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full(qb), q_bytes);
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(sbase + C::OFF_Q + qb * TILE_BYTES),
+            "l"(reinterpret_cast<uint64_t>(&tm_q)), "r"(q_full(qb)), "r"(0), "r"(w.h * g.group), "r"(w.u.tok0), "r"(w.b)
+            : "memory");
+      }
+      ++qn;
+      for (int k = w.k0; k < w.k1; ++k, ++it) {
+        const int st = it % ST;
+        PageLoad l{false, 0};
+        if (lane < n_pages) l = page_of_tile(g, w.b, w.u, w.u.tile(k), lane);
+        const uint32_t loaded = __ballot_sync(0xffffffffu, l.load);
+        ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(st), ((it / ST) & 1) ^ 1u, wc));
+        if (!ok) break;
+        if (lane == 0) {
+          holes[st] = hole_bits(g, loaded);
+          mbar_arrive_expect_tx(k_full(st), __popc(loaded) * page_bytes);
+          mbar_arrive_expect_tx(v_full(st), __popc(loaded) * page_bytes);
+        }
+        __syncwarp();
+        if (l.load) {
+          tma_load_2d(sbase + C::OFF_K + st * TILE_BYTES + lane * page_bytes, &tm_k, k_full(st), w.h * DH, l.row);
+          tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, v_full(st), w.h * DH, l.row);
+        }
+      }
+    } while (ok && chunk_next(cp, w));
+    // Let the last copies land before the CTA may exit.
+    if (qn > 0) mbar_wait_drain(q_full((qn - 1) & 1), ((qn - 1) >> 1) & 1, p.limit_ns);
+    for (int i = max(0, it - ST); i < it; ++i) {
+      mbar_wait_drain(k_full(i % ST), (i / ST) & 1, p.limit_ns);
+      mbar_wait_drain(v_full(i % ST), (i / ST) & 1, p.limit_ns);
+    }
+  } else if (any && warp == C::MMA_WARP) {
+    if (lane == 0) {
+      // ---------------- MMA issuer (as in flash_attn_kernel) ----------------
+      constexpr uint32_t idesc_s = idesc_f16_f32(fa::BQ, BKV, 0, 0);  // Q, K both K-major
+      constexpr uint32_t idesc_o = idesc_f16_f32(fa::BQ, DH, 0, 1);   // P K-major (TMEM), V MN-major
+      const uint64_t q_desc0 = smem_desc_sw128(sbase + C::OFF_Q, 16, 1024);
+      const uint64_t k_desc0 = smem_desc_sw128(sbase + C::OFF_K, 16, 1024);
+      const uint64_t v_desc0 = smem_desc_sw128(sbase + C::OFF_V, TILE_BYTES, 1024);
+      constexpr uint64_t kTileUnits = TILE_BYTES >> 4;
+      const uint32_t s_t = tmem_base + C::S_COL, o_t = tmem_base + C::O_COL, p_t = tmem_base + C::P_COL;
+      int qn = 0, it = 0;
+      bool ok = true;
+      auto issue_pv = [&](int t, bool first) -> bool {
+        const int st = t % ST;
+        if (!mbar_wait(v_full(st), (t / ST) & 1, wc)) return false;
+        if (first && qn > 1 && !mbar_wait(o_free, (qn - 2) & 1, wc)) return false;
+        if (!mbar_wait(p_full, t & 1, wc)) return false;
+        tc_fence_after();
+        const uint64_t vd = v_desc0 + st * kTileUnits;
+#pragma unroll
+        for (int kk = 0; kk < BKV / 16; ++kk)
+          mma_f16_ts(o_t, p_t + kk * 8, vd + kk * 128, idesc_o, (!first || kk > 0) ? 1u : 0u);
+        mma_commit(o_done);
+        mma_commit(kv_empty(st));
+        return true;
+      };
+      do {
+        if (w.k1 <= w.k0) continue;
+        const int qb = qn & 1;
+        if (!mbar_wait(q_full(qb), (qn >> 1) & 1, wc)) break;
+        ++qn;
+        const uint64_t qd = q_desc0 + qb * kTileUnits;
+        for (int k = w.k0; k < w.k1; ++k, ++it) {
+          const int st = it % ST;
+          if (!mbar_wait(k_full(st), (it / ST) & 1, wc) || (it > 0 && !mbar_wait(s_free, (it - 1) & 1, wc))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t kd = k_desc0 + st * kTileUnits;
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk) mma_f16_ss(s_t, qd + kk * 2, kd + kk * 2, idesc_s, kk > 0 ? 1u : 0u);
+          mma_commit(s_full);
+          if (k > w.k0 && !issue_pv(it - 1, k == w.k0 + 1)) {
+            ok = false;
+            break;
+          }
+        }
+        if (!ok || !issue_pv(it - 1, w.k1 == w.k0 + 1)) {
+          ok = false;
+          break;
+        }
+        mma_commit(q_empty(qb));
+      } while (ok && chunk_next(cp, w));
+      mma_commit(drain_bar);
+      mbar_wait_drain(drain_bar, 0, p.limit_ns);
+    }
+  } else if (any) {
+    // ---------------- softmax / correction / epilogue ----------------
+    const uint32_t lane_field = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t s_tmem = tmem_base + C::S_COL + lane_field;
+    const uint32_t o_tmem = tmem_base + C::O_COL + lane_field;
+    const uint32_t p_tmem = tmem_base + C::P_COL + lane_field;
+    const float sl2 = p.scale_log2;
+    const int row = warp * 32 + lane;          // row of the tile == tensor-memory lane
+    const int tok_r = fa::div_c(row, cp.dv_group);  // its token within the tile
+    const int head_r = row - tok_r * g.group;
+    int it = 0;
+    bool ok = true;
+    do {
+      const bool row_ok = tok_r < w.u.ntok;
+      const bool row_out = tok_r < g.tok_per_tile && w.u.tok0 + tok_r < g.t_q;  // valid or padding
+      const int64_t out_row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + tok_r;
+      const int head = w.h * g.group + head_r;
+      __half* out = p.out + out_row * p.out_stride + head * DH;
+      if (w.k1 <= w.k0) {  // no row sees anything (whole units only)
+        if (row_out) {
+#pragma unroll
+          for (int v = 0; v < DH / 8; ++v) reinterpret_cast<uint4*>(out)[v] = make_uint4(0u, 0u, 0u, 0u);
+          if (p.lse != nullptr) p.lse[out_row * g.n_heads + head] = -INFINITY;
+        }
+        continue;
+      }
+      const RowSpan rs = row_ok ? row_span(g, w.s, w.u.tok0 + tok_r + w.s.off) : RowSpan{0, 0, 0};
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int k = w.k0; k < w.k1; ++k) {
+        const int st = it % ST;
+        if (!mbar_wait(k_full(st), (it / ST) & 1, wc)) {  // the producer's hole bits
+          ok = false;
+          break;
+        }
+        const uint32_t hole = holes[st];
+        if (!mbar_wait(s_full, it & 1, wc)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[BKV];
+        {
+          uint32_t r[BKV];
+          tmem_ld128(s_tmem, r);
+#pragma unroll
+          for (int e = 0; e < BKV; ++e) s[e] = __uint_as_float(r[e]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
+
+        const int kv0 = w.u.tile(k) * BKV;
+        const int a = rs.lo - kv0, bnd = rs.hi - kv0, fb = rs.f - kv0;
+        if (row_ok && !((a <= 0 && bnd >= BKV) || fb >= BKV)) {
+          if (a <= 0 && bnd >= BKV / 2 && fb <= bnd) {
+#pragma unroll
+            for (int e = BKV / 2; e < BKV; ++e)
+              if (e >= bnd) s[e] = -INFINITY;
+          } else {
+#pragma unroll
+            for (int e = 0; e < BKV; ++e)
+              if (!((e >= a && e < bnd) || e < fb)) s[e] = -INFINITY;
+          }
+        }
+        if (hole != 0) {
+#pragma unroll
+          for (int e = 0; e < BKV; ++e)
+            if ((hole >> (e / GRANULE)) & 1u) s[e] = -INFINITY;
+        }
+        float mx4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(s[i], s[BKV - 4 + i]);
+#pragma unroll
+        for (int e = 4; e < BKV - 4; e += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx4[i] = fmax3(mx4[i], s[e + i], s[e + 4 + i]);
+        }
+        const float mx_l2 = fmaxf(fmax3(mx4[0], mx4[1], mx4[2]), mx4[3]) * sl2;
+        const bool grow = mx_l2 > m_run + RESCALE_LIMIT;
+        const float m_new = grow ? mx_l2 : m_run;
+        const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
+        const bool first = k == w.k0;
+        if (!first) {
+          if (!mbar_wait(o_done, (it - 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+        }
+        {
+          const float ref = m_new == -INFINITY ? 0.f : m_new;
+          const uint64_t sl2x2 = f2_pack(sl2, sl2), negm2 = f2_pack(-ref, -ref);
+          uint64_t acc2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < BKV / 16; ++c) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s[16 * c + 2 * i], s[16 * c + 2 * i + 1]), sl2x2, negm2), x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              acc2[i & 1] = f2_add(acc2[i & 1], f2_pack(p0, p1));
+              pk[i] = pack_half2(p0, p1);  // P in fp16 for the tensor cores; the sum is not rounded
+            }
+            tmem_st8_async(p_tmem + c * 8, pk);
+          }
+          tmem_wait_st();
+          float sum0, sum1;
+          f2_unpack(f2_add(acc2[0], acc2[1]), sum0, sum1);
+          l_run = l_run * alpha + (sum0 + sum1);
+        }
+        if (!first && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            tmem_ld32(o_tmem + c * 32, r);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
+            tmem_st32(o_tmem + c * 32, r);
+          }
+        }
+        // Values of slots that no row of the tile sees may be anything, and a
+        // weight of zero does not silence NaN: they are cleared in shared memory.
+        const Span& u = w.u;
+        if (hole != 0 || !((kv0 >= u.lo && kv0 + BKV <= u.hi) || kv0 + BKV <= u.f)) {
+          if (!mbar_wait(v_full(st), (it / ST) & 1, wc)) {
+            ok = false;
+            break;
+          }
+          for (int x = row; x < BKV * 8; x += C::SOFTMAX_THREADS) {
+            const int j = x >> 3;
+            if (((hole >> (j / GRANULE)) & 1u) || unseen(u, kv0 + j))
+              *reinterpret_cast<uint4*>(smem + C::OFF_V + st * TILE_BYTES + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+        m_run = m_new;
+        ++it;
+      }
+      if (!ok) break;
+
+      // ---------------- epilogue ----------------
+      if (!mbar_wait(o_done, (it - 1) & 1, wc)) break;
+      tc_fence_after();
+      float l_fin = row_ok ? l_run : 0.f;
+      if (w.whole && p.sinks != nullptr && l_fin > 0.f) l_fin += ex2_approx(__ldg(p.sinks + head) * kLog2e - m_run);
+      const float inv = l_fin > 0.f ? 1.f / l_fin : 0.f;
+      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + w.slot) * p.rows_cap + row;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32];
+        tmem_ld32(o_tmem + c * 32, r);
+        if (c == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+        }
+        if (w.whole) {
+          if (!row_out) continue;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint4 x;
+            x.x = pack_half2(__uint_as_float(r[8 * v + 0]) * inv, __uint_as_float(r[8 * v + 1]) * inv);
+            x.y = pack_half2(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
+            x.z = pack_half2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
+            x.w = pack_half2(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv);
+            // a padding row's products may be NaN
+            reinterpret_cast<uint4*>(out + c * 32)[v] = l_fin > 0.f ? x : make_uint4(0u, 0u, 0u, 0u);
+          }
+        } else if (row_ok) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            reinterpret_cast<float4*>(p.ws_o + part * DH + c * 32)[v] =
+                make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]), __uint_as_float(r[4 * v + 2]),
+                            __uint_as_float(r[4 * v + 3]));
+        }
+      }
+      if (w.whole) {
+        if (row_out && p.lse != nullptr)
+          p.lse[out_row * g.n_heads + head] = l_fin > 0.f ? m_run * kLn2 + logf(l_fin) : -INFINITY;
+      } else if (row_ok) {
+        p.ws_ml[part] = make_float2(m_run, l_run);
+      }
+    } while (chunk_next(cp, w));
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace pg
+}  // namespace sea

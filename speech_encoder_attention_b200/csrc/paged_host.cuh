@@ -2,7 +2,7 @@
 // checks (pure arithmetic, before any CUDA call), launch plans and launches.
 // Included by attn_api.cu inside its unnamed namespace.
 
-constexpr int kMaxGroup = 32;  // query heads per K/V head
+constexpr int kMaxGroup = 128; // query heads per K/V head
 
 bool misaligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) != 0; }
 
@@ -86,6 +86,25 @@ bool encode_pages(CUtensorMap* m, const attn_paged_kv& c, const attn_mat& pool) 
          CUDA_SUCCESS;
 }
 
+// (column, head, token, sequence) view of the queries: a tile is `group` heads
+// of tok_per_tile tokens, one 128-byte row each.
+bool encode_paged_q(CUtensorMap* m, const attn_mat& q, int batch, int t_q, int n_heads, int group, int tok_per_tile) {
+  auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(q.row_stride) * 2;
+  cuuint64_t dims[4] = {sea::pg::DH, static_cast<cuuint64_t>(n_heads), static_cast<cuuint64_t>(t_q),
+                        static_cast<cuuint64_t>(batch)};
+  cuuint64_t strides[3] = {sea::pg::DH * 2, row, row * t_q};
+  cuuint32_t box[4] = {sea::pg::DH, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tok_per_tile), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, q.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Chunks with at least this many units per CTA are walked unit by unit.
+constexpr int kWholeUnitsPerCta = 4;
+
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
   int tok_per_tile, q_tiles;
@@ -96,7 +115,9 @@ struct PagedPlan {
 PagedPlan plan_paged(int t_q, int n_heads, int kv_heads, int num_sms) {
   const int group = n_heads / kv_heads;
   PagedPlan pl{};
-  pl.rows_cap = static_cast<int64_t>(t_q) * group <= 16 ? 16 : 32;
+  // Up to 32 rows per K/V head: paged_step_kernel with 16 or 32 rows per tile.
+  const int64_t rows = static_cast<int64_t>(t_q) * group;
+  pl.rows_cap = rows <= 16 ? 16 : rows <= 32 ? 32 : sea::fa::BQ;
   pl.tok_per_tile = std::max(1, std::min(t_q, pl.rows_cap / group));
   pl.q_tiles = ceil_div(t_q, pl.tok_per_tile);
   pl.parts = std::max(1, 2 * num_sms / kv_heads);
@@ -180,11 +201,27 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   p.err = dev->err;
   p.limit_ns = sea::kDefaultTimeoutNs;
   using sea::pg::StepCfg;
-  cudaError_t err = pl.rows_cap == 16
-                        ? launch_pdl(sea::pg::paged_step_kernel<1>, dim3(pl.ctas), dim3(StepCfg<1>::THREADS),
-                                     StepCfg<1>::SMEM_BYTES, stream, tk, tv, p)
-                        : launch_pdl(sea::pg::paged_step_kernel<2>, dim3(pl.ctas), dim3(StepCfg<2>::THREADS),
-                                     StepCfg<2>::SMEM_BYTES, stream, tk, tv, p);
+  cudaError_t err;
+  if (pl.rows_cap == sea::fa::BQ) {
+    CUtensorMap tq;
+    if (!encode_paged_q(&tq, q, batch, t_q, n_heads, p.g.group, pl.tok_per_tile)) return ATTN_ERR_CUDA;
+    sea::pg::ChunkParams cp{};
+    cp.s = p;
+    cp.units = static_cast<int>(units);
+    cp.cut = units < int64_t(kWholeUnitsPerCta) * 2 * dev->num_sms ? 1 : 0;
+    cp.dv_group = make_divc(p.g.group);
+    cp.dv_heads = make_divc(cache.n_kv_heads);
+    cp.dv_bh = make_divc(batch * cache.n_kv_heads);
+    const int grid = cp.cut ? pl.ctas : static_cast<int>(std::min<int64_t>(units, int64_t(2) * dev->num_sms));
+    err = launch_pdl(sea::pg::paged_chunk_kernel, dim3(grid), dim3(sea::pg::ChunkCfg::THREADS),
+                     sea::pg::ChunkCfg::SMEM_BYTES, stream, tq, tk, tv, cp);
+    if (!cp.cut) return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  } else {
+    err = pl.rows_cap == 16 ? launch_pdl(sea::pg::paged_step_kernel<1>, dim3(pl.ctas), dim3(StepCfg<1>::THREADS),
+                                         StepCfg<1>::SMEM_BYTES, stream, tk, tv, p)
+                            : launch_pdl(sea::pg::paged_step_kernel<2>, dim3(pl.ctas), dim3(StepCfg<2>::THREADS),
+                                         StepCfg<2>::SMEM_BYTES, stream, tk, tv, p);
+  }
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
   const unsigned parts = static_cast<unsigned>(ceil_div(pl.rows_cap, 4 * sea::pg::COMBINE_WARPS));
   if (launch_pdl(sea::pg::paged_combine_kernel, dim3(static_cast<unsigned>(units), parts),

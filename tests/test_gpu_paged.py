@@ -54,6 +54,8 @@ CASES = {
     "chunk_group": dict(lens=[140], t_q=41, heads=10, kv=2, page=64),
     "chunk_open": dict(lens=[180, 20], t_q=50, heads=2, kv=2, page=128, causal=False, q_lens=[45, 50]),
     "many_heads_on_one": dict(lens=[150, 20], t_q=1, heads=20, kv=1, page=16),
+    "group_of_40": dict(lens=[150, 20], t_q=2, heads=40, kv=1, page=16),
+    "group_of_128": dict(lens=[130], t_q=3, heads=128, kv=1, page=16),
     "odd_group": dict(lens=[130, 260], t_q=30, heads=7, kv=1, page=16),
 }
 
