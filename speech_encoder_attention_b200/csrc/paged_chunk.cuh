@@ -23,9 +23,24 @@
 namespace sea {
 namespace pg {
 
+// A unit as the producer hands it to the other roles, in shared memory: that
+// keeps the walk's state out of the softmax threads' registers. The entry of
+// unit n is free again once the producer may load Q of unit n + 4: Q of unit
+// n + 2 has then been used up, so every role has left unit n.
+struct ChunkUnit {
+  int b, h, tok0, ntok;
+  int kv, off;             // slots in use, position of the chunk's row 0
+  int lo, hi, f;           // what any row of the tile sees
+  int n_first, t_lo;       // key tile k is k (k < n_first) or t_lo + k - n_first
+  int k0, k1;              // key tiles of this unit; k1 = 0 ends the walk
+  int whole, slot;
+};
+constexpr int kUnitRing = 4;
+
 struct ChunkCfg : fa::CfgT<2> {
   static constexpr int OFF_HOLES = OFF_MISC + 8;
-  static constexpr int SMEM_BYTES = 1024 + OFF_HOLES + 4 * STAGES;
+  static constexpr int OFF_UNITS = OFF_HOLES + 4 * STAGES;
+  static constexpr int SMEM_BYTES = 1024 + OFF_UNITS + kUnitRing * static_cast<int>(sizeof(ChunkUnit));
 };
 
 struct ChunkParams {
@@ -76,6 +91,19 @@ __device__ __forceinline__ bool chunk_next(const ChunkParams& p, ChunkWalk& w) {
   return true;
 }
 
+// One warp: the rows of a query tile that sees nothing.
+__device__ __forceinline__ void zero_rows(const StepParams& p, int b, int h, int tok0) {
+  const Geo& g = p.g;
+  const int rows = min(g.tok_per_tile, g.t_q - tok0) * g.group;
+  for (int x = threadIdx.x & 31; x < rows * 8; x += 32) {
+    const int r = x >> 3;
+    const int64_t row = static_cast<int64_t>(b) * g.t_q + tok0 + r / g.group;
+    const int head = h * g.group + r % g.group;
+    reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * DH)[x & 7] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse != nullptr && (x & 7) == 0) p.lse[row * g.n_heads + head] = -INFINITY;
+  }
+}
+
 __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const ChunkParams cp) {
@@ -99,6 +127,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
   volatile uint32_t* holes = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_HOLES);
+  ChunkUnit* units = reinterpret_cast<ChunkUnit*>(smem + C::OFF_UNITS);
   const StepParams& p = cp.s;
   const Geo& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,21 +166,39 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
   griddep_launch_dependents();
   const WaitCtl wc{abort_flag, p.err, p.limit_ns};
 
-  ChunkWalk w;
-  const bool any = chunk_start(cp, w);
-  if (any && warp == C::PRODUCER_WARP) {
+  if (warp == C::PRODUCER_WARP) {
     // ---------------- TMA producer (whole warp: lane i loads page i of a tile) ----------------
     const int n_pages = pages_per_tile(g);
     const uint32_t page_bytes = TILE_BYTES / n_pages;
     const uint32_t q_bytes = static_cast<uint32_t>(g.tok_per_tile * g.group) * DH * 2;
     int qn = 0, it = 0;
-    bool ok = true;
-    do {
-      if (w.k1 <= w.k0) continue;
+    ChunkWalk w;
+    bool more = chunk_start(cp, w), ok = true;
+    for (; more; more = ok && chunk_next(cp, w)) {
+      if (w.k1 <= w.k0) {  // no row sees anything (whole units only)
+        zero_rows(p, w.b, w.h, w.u.tok0);
+        continue;
+      }
       const int qb = qn & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(q_empty(qb), ((qn >> 1) & 1) ^ 1u, wc));
       if (!ok) break;
       if (lane == 0) {
+        ChunkUnit& u = units[qn % kUnitRing];
+        u.b = w.b;
+        u.h = w.h;
+        u.tok0 = w.u.tok0;
+        u.ntok = w.u.ntok;
+        u.kv = w.s.kv;
+        u.off = w.s.off;
+        u.lo = w.u.lo;
+        u.hi = w.u.hi;
+        u.f = w.u.f;
+        u.n_first = w.u.n_first;
+        u.t_lo = w.u.t_lo;
+        u.k0 = w.k0;
+        u.k1 = w.k1;
+        u.whole = w.whole;
+        u.slot = w.slot;
         mbar_arrive_expect_tx(q_full(qb), q_bytes);
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
@@ -178,14 +225,18 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
           tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, v_full(st), w.h * DH, l.row);
         }
       }
-    } while (ok && chunk_next(cp, w));
+    }
+    if (ok && mbar_wait(q_empty(qn & 1), ((qn >> 1) & 1) ^ 1u, wc) && lane == 0) {  // the end of the walk
+      units[qn % kUnitRing].k1 = 0;
+      mbar_arrive(q_full(qn & 1));
+    }
     // Let the last copies land before the CTA may exit.
     if (qn > 0) mbar_wait_drain(q_full((qn - 1) & 1), ((qn - 1) >> 1) & 1, p.limit_ns);
     for (int i = max(0, it - ST); i < it; ++i) {
       mbar_wait_drain(k_full(i % ST), (i / ST) & 1, p.limit_ns);
       mbar_wait_drain(v_full(i % ST), (i / ST) & 1, p.limit_ns);
     }
-  } else if (any && warp == C::MMA_WARP) {
+  } else if (warp == C::MMA_WARP) {
     if (lane == 0) {
       // ---------------- MMA issuer (as in flash_attn_kernel) ----------------
       constexpr uint32_t idesc_s = idesc_f16_f32(fa::BQ, BKV, 0, 0);  // Q, K both K-major
@@ -211,13 +262,14 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         mma_commit(kv_empty(st));
         return true;
       };
-      do {
-        if (w.k1 <= w.k0) continue;
+      while (ok) {
         const int qb = qn & 1;
         if (!mbar_wait(q_full(qb), (qn >> 1) & 1, wc)) break;
+        const int k0 = units[qn % kUnitRing].k0, k1 = units[qn % kUnitRing].k1;
+        if (k1 == 0) break;
         ++qn;
         const uint64_t qd = q_desc0 + qb * kTileUnits;
-        for (int k = w.k0; k < w.k1; ++k, ++it) {
+        for (int k = k0; k < k1; ++k, ++it) {
           const int st = it % ST;
           if (!mbar_wait(k_full(st), (it / ST) & 1, wc) || (it > 0 && !mbar_wait(s_free, (it - 1) & 1, wc))) {
             ok = false;
@@ -228,21 +280,18 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) mma_f16_ss(s_t, qd + kk * 2, kd + kk * 2, idesc_s, kk > 0 ? 1u : 0u);
           mma_commit(s_full);
-          if (k > w.k0 && !issue_pv(it - 1, k == w.k0 + 1)) {
+          if (k > k0 && !issue_pv(it - 1, k == k0 + 1)) {
             ok = false;
             break;
           }
         }
-        if (!ok || !issue_pv(it - 1, w.k1 == w.k0 + 1)) {
-          ok = false;
-          break;
-        }
+        if (!ok || !issue_pv(it - 1, k1 == k0 + 1)) break;
         mma_commit(q_empty(qb));
-      } while (ok && chunk_next(cp, w));
+      }
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0, p.limit_ns);
     }
-  } else if (any) {
+  } else {
     // ---------------- softmax / correction / epilogue ----------------
     const uint32_t lane_field = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t s_tmem = tmem_base + C::S_COL + lane_field;
@@ -254,23 +303,16 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
     const int head_r = row - tok_r * g.group;
     int it = 0;
     bool ok = true;
-    do {
-      const bool row_ok = tok_r < w.u.ntok;
-      const bool row_out = tok_r < g.tok_per_tile && w.u.tok0 + tok_r < g.t_q;  // valid or padding
-      const int64_t out_row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + tok_r;
-      const int head = w.h * g.group + head_r;
-      __half* out = p.out + out_row * p.out_stride + head * DH;
-      if (w.k1 <= w.k0) {  // no row sees anything (whole units only)
-        if (row_out) {
-#pragma unroll
-          for (int v = 0; v < DH / 8; ++v) reinterpret_cast<uint4*>(out)[v] = make_uint4(0u, 0u, 0u, 0u);
-          if (p.lse != nullptr) p.lse[out_row * g.n_heads + head] = -INFINITY;
-        }
-        continue;
-      }
-      const RowSpan rs = row_ok ? row_span(g, w.s, w.u.tok0 + tok_r + w.s.off) : RowSpan{0, 0, 0};
+    for (int n = 0; ok; ++n) {
+      if (!mbar_wait(q_full(n & 1), (n >> 1) & 1, wc)) break;
+      const ChunkUnit& u = units[n % kUnitRing];
+      const int k0 = u.k0, k1 = u.k1;
+      if (k1 == 0) break;
+      const bool row_ok = tok_r < u.ntok;
+      const RowSpan rs = row_ok ? row_span(g, Seq{0, u.kv, 0}, u.tok0 + tok_r + u.off) : RowSpan{0, 0, 0};
+      const int n_first = u.n_first, t_lo = u.t_lo;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int k = w.k0; k < w.k1; ++k) {
+      for (int k = k0; k < k1; ++k) {
         const int st = it % ST;
         if (!mbar_wait(k_full(st), (it / ST) & 1, wc)) {  // the producer's hole bits
           ok = false;
@@ -293,18 +335,25 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
 
-        const int kv0 = w.u.tile(k) * BKV;
+        const int kv0 = (k < n_first ? k : t_lo + k - n_first) * BKV;
         const int a = rs.lo - kv0, bnd = rs.hi - kv0, fb = rs.f - kv0;
+        // Hidden: [fb, a) and from max(bnd, fb) on. Three separate loops: one
+        // with both conditions spills.
         if (row_ok && !((a <= 0 && bnd >= BKV) || fb >= BKV)) {
-          if (a <= 0 && bnd >= BKV / 2 && fb <= bnd) {
-#pragma unroll
-            for (int e = BKV / 2; e < BKV; ++e)
-              if (e >= bnd) s[e] = -INFINITY;
-          } else {
+          const int top = max(bnd, fb);
+          if (a > max(fb, 0)) {
 #pragma unroll
             for (int e = 0; e < BKV; ++e)
-              if (!((e >= a && e < bnd) || e < fb)) s[e] = -INFINITY;
+              if (e >= fb && e < a) s[e] = -INFINITY;
           }
+          if (top < BKV / 2) {
+#pragma unroll
+            for (int e = 0; e < BKV / 2; ++e)
+              if (e >= top) s[e] = -INFINITY;
+          }
+#pragma unroll
+          for (int e = BKV / 2; e < BKV; ++e)
+            if (e >= top) s[e] = -INFINITY;
         }
         if (hole != 0) {
 #pragma unroll
@@ -323,7 +372,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         const bool grow = mx_l2 > m_run + RESCALE_LIMIT;
         const float m_new = grow ? mx_l2 : m_run;
         const float alpha = grow ? ex2_approx(m_run - m_new) : 1.f;
-        const bool first = k == w.k0;
+        const bool first = k == k0;
         if (!first) {
           if (!mbar_wait(o_done, (it - 1) & 1, wc)) {
             ok = false;
@@ -365,7 +414,6 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         }
         // Values of slots that no row of the tile sees may be anything, and a
         // weight of zero does not silence NaN: they are cleared in shared memory.
-        const Span& u = w.u;
         if (hole != 0 || !((kv0 >= u.lo && kv0 + BKV <= u.hi) || kv0 + BKV <= u.f)) {
           if (!mbar_wait(v_full(st), (it / ST) & 1, wc)) {
             ok = false;
@@ -373,7 +421,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
           }
           for (int x = row; x < BKV * 8; x += C::SOFTMAX_THREADS) {
             const int j = x >> 3;
-            if (((hole >> (j / GRANULE)) & 1u) || unseen(u, kv0 + j))
+            if (((hole >> (j / GRANULE)) & 1u) || !((kv0 + j >= u.lo && kv0 + j < u.hi) || kv0 + j < u.f))
               *reinterpret_cast<uint4*>(smem + C::OFF_V + st * TILE_BYTES + x * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -389,10 +437,15 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
       // ---------------- epilogue ----------------
       if (!mbar_wait(o_done, (it - 1) & 1, wc)) break;
       tc_fence_after();
+      const bool whole = u.whole != 0;
+      const bool row_out = tok_r < g.tok_per_tile && u.tok0 + tok_r < g.t_q;  // valid or padding
+      const int64_t out_row = static_cast<int64_t>(u.b) * g.t_q + u.tok0 + tok_r;
+      const int head = u.h * g.group + head_r;
+      __half* out = p.out + out_row * p.out_stride + head * DH;
       float l_fin = row_ok ? l_run : 0.f;
-      if (w.whole && p.sinks != nullptr && l_fin > 0.f) l_fin += ex2_approx(__ldg(p.sinks + head) * kLog2e - m_run);
+      if (whole && row_ok && p.sinks != nullptr && l_fin > 0.f) l_fin += ex2_approx(__ldg(p.sinks + head) * kLog2e - m_run);
       const float inv = l_fin > 0.f ? 1.f / l_fin : 0.f;
-      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + w.slot) * p.rows_cap + row;
+      const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + u.slot) * p.rows_cap + row;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t r[32];
@@ -402,7 +455,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
           __syncwarp();
           if (lane == 0) mbar_arrive(o_free);
         }
-        if (w.whole) {
+        if (whole) {
           if (!row_out) continue;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
@@ -422,13 +475,13 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
                             __uint_as_float(r[4 * v + 3]));
         }
       }
-      if (w.whole) {
+      if (whole) {
         if (row_out && p.lse != nullptr)
           p.lse[out_row * g.n_heads + head] = l_fin > 0.f ? m_run * kLn2 + logf(l_fin) : -INFINITY;
       } else if (row_ok) {
         p.ws_ml[part] = make_float2(m_run, l_run);
       }
-    } while (chunk_next(cp, w));
+    }
   }
 
   __syncwarp();
