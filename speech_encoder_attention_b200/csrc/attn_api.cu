@@ -136,6 +136,12 @@ attn_status device_info(DeviceInfo** out) {
                              sea::pg::StepCfg<1>::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::pg::paged_step_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::pg::StepCfg<2>::SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(sea::pg::paged_weights_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sea::pg::WeightCfg<16>::SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(sea::pg::paged_weights_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sea::pg::WeightCfg<32>::SMEM_BYTES) != cudaSuccess ||
+        cudaFuncSetAttribute(sea::pg::paged_weights_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             sea::pg::WeightCfg<128>::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::pg::paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::pg::ChunkCfg::SMEM_BYTES) != cudaSuccess ||
         !set_attention_smem<2>() || !set_attention_smem<4>())

@@ -12,7 +12,8 @@
 //   warp 5     tcgen05.mma issuer: S = Q K^T, then O += P V.
 // Two ways to deal out the work. With many units (sequence, head, query tile)
 // each CTA walks whole units, the ones at the end of the prompts, which see
-// most, first. With few, the key tiles of all units are cut into equal parts as
+// most, first, every other round in reverse order of the CTAs so that the shares
+// come out even. With few, the key tiles of all units are cut into equal parts as
 // in paged_step_kernel, and paged_combine_kernel merges what was cut.
 #pragma once
 
@@ -50,10 +51,10 @@ struct ChunkParams {
   fa::DivC dv_group, dv_heads, dv_bh;  // by group, kv_heads, batch * kv_heads
 };
 
-// The units of a CTA: a Walk over its part, or units blockIdx.x, + gridDim.x, ...
-// with the last query tiles of all sequences and heads first.
+// The units of a CTA: a Walk over its part, or one unit of each round of
+// gridDim.x, with the last query tiles of all sequences and heads first.
 struct ChunkWalk : Walk {
-  int h, unit;
+  int h, unit, round;
 };
 
 __device__ __forceinline__ void chunk_unit(const ChunkParams& p, ChunkWalk& w) {
@@ -77,6 +78,7 @@ __device__ __forceinline__ bool chunk_start(const ChunkParams& p, ChunkWalk& w) 
     w.h = blockIdx.x % g.kv_heads;
     return walk_start(g, w, blockIdx.x / g.kv_heads, p.s.parts, p.s.least);
   }
+  w.round = 0;
   w.unit = blockIdx.x;
   if (w.unit >= p.units) return false;
   chunk_unit(p, w);
@@ -85,8 +87,9 @@ __device__ __forceinline__ bool chunk_start(const ChunkParams& p, ChunkWalk& w) 
 
 __device__ __forceinline__ bool chunk_next(const ChunkParams& p, ChunkWalk& w) {
   if (p.cut) return walk_next(p.s.g, w);
-  w.unit += gridDim.x;
-  if (w.unit >= p.units) return false;
+  ++w.round;
+  w.unit = w.round * gridDim.x + (w.round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  if (w.unit >= p.units) return false;  // of the last, incomplete round
   chunk_unit(p, w);
   return true;
 }
@@ -200,11 +203,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         u.whole = w.whole;
         u.slot = w.slot;
         mbar_arrive_expect_tx(q_full(qb), q_bytes);
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(sbase + C::OFF_Q + qb * TILE_BYTES),
-            "l"(reinterpret_cast<uint64_t>(&tm_q)), "r"(q_full(qb)), "r"(0), "r"(w.h * g.group), "r"(w.u.tok0), "r"(w.b)
-            : "memory");
+        tma_load_4d(sbase + C::OFF_Q + qb * TILE_BYTES, &tm_q, q_full(qb), 0, w.h * g.group, w.u.tok0, w.b);
       }
       ++qn;
       for (int k = w.k0; k < w.k1; ++k, ++it) {
@@ -443,8 +442,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
       const int head = u.h * g.group + head_r;
       __half* out = p.out + out_row * p.out_stride + head * DH;
       float l_fin = row_ok ? l_run : 0.f;
-      if (whole && row_ok && p.sinks != nullptr && l_fin > 0.f) l_fin += ex2_approx(__ldg(p.sinks + head) * kLog2e - m_run);
-      const float inv = l_fin > 0.f ? 1.f / l_fin : 0.f;
+      if (whole && row_ok && p.sinks != nullptr && l_fin != 0.f) l_fin += ex2_approx(__ldg(p.sinks + head) * kLog2e - m_run);
+      const float inv = l_fin != 0.f ? 1.f / l_fin : 0.f;
       const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + u.slot) * p.rows_cap + row;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
             x.z = pack_half2(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
             x.w = pack_half2(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv);
             // a padding row's products may be NaN
-            reinterpret_cast<uint4*>(out + c * 32)[v] = l_fin > 0.f ? x : make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(out + c * 32)[v] = l_fin != 0.f ? x : make_uint4(0u, 0u, 0u, 0u);
           }
         } else if (row_ok) {
 #pragma unroll
@@ -477,7 +476,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
       }
       if (whole) {
         if (row_out && p.lse != nullptr)
-          p.lse[out_row * g.n_heads + head] = l_fin > 0.f ? m_run * kLn2 + logf(l_fin) : -INFINITY;
+          p.lse[out_row * g.n_heads + head] = l_fin != 0.f ? m_run * kLn2 + logf(l_fin) : -INFINITY;
       } else if (row_ok) {
         p.ws_ml[part] = make_float2(m_run, l_run);
       }

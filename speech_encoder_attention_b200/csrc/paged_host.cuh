@@ -223,9 +223,11 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
                                          StepCfg<2>::SMEM_BYTES, stream, tk, tv, p);
   }
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
-  const unsigned parts = static_cast<unsigned>(ceil_div(pl.rows_cap, 4 * sea::pg::COMBINE_WARPS));
-  if (launch_pdl(sea::pg::paged_combine_kernel, dim3(static_cast<unsigned>(units), parts),
-                 dim3(32 * sea::pg::COMBINE_WARPS), 0, stream, p) != cudaSuccess)
+  const int unit_rows = pl.tok_per_tile * p.g.group;
+  const int rows_log2 = log2_of(std::min(unit_rows, 32));
+  if (launch_pdl(sea::pg::paged_combine_kernel,
+                 dim3(static_cast<unsigned>(units), static_cast<unsigned>(ceil_div(unit_rows, 1 << rows_log2))),
+                 dim3(sea::pg::COMBINE_THREADS), 0, stream, p, rows_log2) != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }
@@ -252,28 +254,35 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
   sea::pg::WeightParams p{};
   p.g = paged_geo(cache, batch, t_q, n_heads, mask);
-  p.q = static_cast<const __half*>(q.ptr);
-  p.q_stride = q.row_stride;
-  p.k = static_cast<const __half*>(cache.k.ptr);
-  p.k_stride = cache.k.row_stride;
+  const int64_t group_rows = static_cast<int64_t>(t_q) * p.g.group;
+  // Rows of a query tile: as few as hold the chunk, a whole number of tokens.
+  const int n = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : 128;
+  p.g.tok_per_tile = static_cast<int>(std::min<int64_t>(t_q, n / p.g.group));
   p.lse = lse;
   p.w_in = w_in;
   p.w_out = w_out;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.dv_group = make_divc(p.g.group);
+  p.err = dev->err;
+  p.limit_ns = sea::kDefaultTimeoutNs;
+  CUtensorMap tq, tk;
+  if (!encode_paged_q(&tq, q, batch, t_q, n_heads, p.g.group, p.g.tok_per_tile) || !encode_pages(&tk, cache, cache.k))
+    return ATTN_ERR_CUDA;
   const int tiles = ceil_div(p.g.cap, sea::pg::BKV);
-  const int64_t group_rows = static_cast<int64_t>(t_q) * p.g.group;
-  const bool few = group_rows <= 32;
   // Ranks of a key tile's cluster: enough CTAs for about three per SM, as long
   // as every rank has an item.
-  const int64_t items = few ? cache.n_kv_heads
-                            : static_cast<int64_t>(cache.n_kv_heads) * ceil_div(group_rows, sea::pg::WEIGHT_ROWS) / 2;
+  const int64_t items = static_cast<int64_t>(cache.n_kv_heads) * ceil_div(t_q, p.g.tok_per_tile);
+  if (items > INT32_MAX / 8) return ATTN_ERR_INVALID;
   int ranks = 1;
   while (ranks < 8 && 2 * ranks <= items && static_cast<int64_t>(tiles) * batch * ranks < 3 * dev->num_sms) ranks *= 2;
-  const dim3 grid(ranks, tiles, batch), block(32 * sea::pg::WEIGHT_WARPS);
+  const dim3 grid(ranks, batch, tiles);
+  auto launch = [&](auto kernel, int threads, int smem) {
+    return launch_pdl_cluster(kernel, grid, dim3(threads), smem, stream, static_cast<unsigned>(ranks), tq, tk, p);
+  };
+  using sea::pg::WeightCfg;
   const cudaError_t err =
-      few ? launch_pdl_cluster(sea::pg::paged_weights_kernel<1>, grid, block, 0, stream, ranks, p)
-          : launch_pdl_cluster(sea::pg::paged_weights_kernel<2>, grid, block, 0, stream, ranks, p);
+      n == 16   ? launch(sea::pg::paged_weights_kernel<16>, WeightCfg<16>::THREADS, WeightCfg<16>::SMEM_BYTES)
+      : n == 32 ? launch(sea::pg::paged_weights_kernel<32>, WeightCfg<32>::THREADS, WeightCfg<32>::SMEM_BYTES)
+                : launch(sea::pg::paged_weights_kernel<128>, WeightCfg<128>::THREADS, WeightCfg<128>::SMEM_BYTES);
   return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

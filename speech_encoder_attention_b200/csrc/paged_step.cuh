@@ -338,24 +338,24 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float mw[3], lw[3];
-            float mx = l_run[m][e] > 0.f ? m_run[m][e] : -INFINITY;
+            float mx = l_run[m][e] != 0.f ? m_run[m][e] : -INFINITY;
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
               const float* src = merge_buf + i * C::MERGE_WARP + MT * 1024;
               mw[i] = src[(m * 4 + e) * 32 + lane];
               lw[i] = src[(m * 4 + 2 + e) * 32 + lane];
-              if (lw[i] > 0.f) mx = fmaxf(mx, mw[i]);
+              if (lw[i] != 0.f) mx = fmaxf(mx, mw[i]);
             }
-            const float own = l_run[m][e] > 0.f ? ex2_approx(m_run[m][e] - mx) : 0.f;
+            const float own = l_run[m][e] != 0.f ? ex2_approx(m_run[m][e] - mx) : 0.f;
             float l = l_run[m][e] * own;
 #pragma unroll
             for (int d = 0; d < 8; ++d) {
-              o[m][d][2 * e] = own > 0.f ? o[m][d][2 * e] * own : 0.f;
-              o[m][d][2 * e + 1] = own > 0.f ? o[m][d][2 * e + 1] * own : 0.f;
+              o[m][d][2 * e] = own != 0.f ? o[m][d][2 * e] * own : 0.f;
+              o[m][d][2 * e + 1] = own != 0.f ? o[m][d][2 * e + 1] * own : 0.f;
             }
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
-              if (lw[i] > 0.f) {
+              if (lw[i] != 0.f) {
                 const float wgt = ex2_approx(mw[i] - mx);
                 l += lw[i] * wgt;
                 const float* src = merge_buf + i * C::MERGE_WARP + m * 1024;
@@ -371,15 +371,15 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
               if (w.whole) {
                 const int64_t row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + r / g.group;
                 const int head = h * g.group + r % g.group;
-                if (p.sinks != nullptr && l > 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                if (p.sinks != nullptr && l != 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
+                const float inv = l != 0.f ? 1.f / l : 0.f;
                 __half* dst = p.out + row * p.out_stride + head * DH + c2;
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
                   *reinterpret_cast<uint32_t*>(dst + 8 * d) =
-                      l > 0.f ? pack_half2(o[m][d][2 * e] * inv, o[m][d][2 * e + 1] * inv) : 0u;
+                      l != 0.f ? pack_half2(o[m][d][2 * e] * inv, o[m][d][2 * e + 1] * inv) : 0u;
                 if (p.lse != nullptr && c2 == 0)
-                  p.lse[row * g.n_heads + head] = l > 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+                  p.lse[row * g.n_heads + head] = l != 0.f ? mx * kLn2 + logf(l) : -INFINITY;
               } else {
                 const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + w.slot) * p.rows_cap + r;
                 float2* dst = reinterpret_cast<float2*>(p.ws_o + part * DH + c2);
@@ -399,16 +399,20 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
   __syncthreads();
 }
 
-// Merges the partials of cut units and writes the rows that no CTA holds:
-// one warp per row (token, query head) of a unit, block (unit, group of rows).
+// Merges the partials of cut units and writes the rows that no CTA holds.
 //   M = max_s m_s,  L = sum_s l_s 2^(m_s - M) [+ 2^(sink log2e - M)],
 //   o = sum_s O_s 2^(m_s - M) / L.
-// Rows without a visible slot, and padding rows, are zero with lse = -inf.
-// Bound by its latency: the partials lie in L2.
-constexpr int COMBINE_WARPS = 8;
+// Rows without a visible slot (l = 0), and padding rows, are zero with lse = -inf.
+// Bound by its latency (the partials lie in L2), so a block of 256 threads takes
+// `rows` rows of a unit, 8 threads per row and group of parts, each 8 columns:
+// the 32 / rows groups of a row read their parts at the same time and meet in
+// shared memory.
+constexpr int COMBINE_THREADS = 256;
 
-__global__ void __launch_bounds__(32 * COMBINE_WARPS, 4)
-    paged_combine_kernel(const StepParams p) {
+__global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const StepParams p, int rows_log2) {
+  __shared__ long long sum_all[8], sum_before[8];
+  __shared__ float sh_o[32][68];   // [row x group][64 columns, padded]
+  __shared__ float2 sh_ml[32];
   const Geo& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   griddep_wait();
@@ -420,70 +424,105 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 4)
   const Seq s = seq_of(g, b);
   const Span u = span_of(g, s, qt);
   const int rows_out = min(g.tok_per_tile, g.t_q - u.tok0) * g.group;  // valid and padding rows
-  const int rows = u.ntok * g.group;
-  long long u0 = 0, per = 1;
-  bool cut = false;
-  if (u.n > 0) {
-    per = share_of(tiles_before(g, g.batch), p.parts, p.least);
-    u0 = tiles_before(g, b) + tiles_before_q(g, s, qt);
-    cut = u0 / per != (u0 + u.n - 1) / per;
+  const int rows = u.n > 0 ? u.ntok * g.group : 0;
+  // Where the unit lies in the line of key tiles: every warp takes a share of
+  // the (sequence, query tile) entries.
+  long long all = 0, before = 0;
+  const int entries = g.batch * g.q_tiles;
+  for (int e = threadIdx.x; e < entries; e += COMBINE_THREADS) {
+    const int eb = e / g.q_tiles, eq = e - eb * g.q_tiles;
+    const int n = span_of(g, seq_of(g, eb), eq).n;
+    all += n;
+    if (eb < b || (eb == b && eq < qt)) before += n;
   }
-  const int c0 = static_cast<int>(u0 / per), c1 = u.n > 0 ? static_cast<int>((u0 + u.n - 1) / per) : 0;
-  const bool c0_first = u0 == per * c0;
-  for (int r = blockIdx.y * COMBINE_WARPS + warp; r < rows_out; r += gridDim.y * COMBINE_WARPS) {
-    const int64_t row = static_cast<int64_t>(b) * g.t_q + u.tok0 + r / g.group;
-    const int head = h * g.group + r % g.group;
-    const bool filled = r < rows && u.n > 0;
-    if (filled && !cut) continue;  // written by the CTA that holds the unit
-    float l = 0.f, o0 = 0.f, o1 = 0.f, mmax = -INFINITY;
-    if (filled) {
-      const int parts = c1 - c0 + 1;
-      auto slot_of = [&](int i) -> int64_t {
-        const int64_t c = static_cast<int64_t>(c0 + i) * g.kv_heads + h;
-        return (2 * c + (i == 0 && !c0_first ? 1 : 0)) * p.rows_cap + r;
-      };
-      for (int i0 = 0; i0 < parts; i0 += 32) {
-        float m = -INFINITY;
-        if (i0 + lane < parts) {
-          const float2 ml = p.ws_ml[slot_of(i0 + lane)];
-          if (ml.y > 0.f) m = ml.x;
-        }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        mmax = fmaxf(mmax, m);
-      }
-      if (mmax != -INFINITY) {
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-          float wgt = 0.f, lw = 0.f;
-          if (i0 + lane < parts) {
-            const float2 ml = p.ws_ml[slot_of(i0 + lane)];
-            if (ml.y > 0.f) {
-              wgt = ex2_approx(ml.x - mmax);
-              lw = ml.y * wgt;
-            }
-          }
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  if (lane == 0) {
+    sum_all[warp] = all;
+    sum_before[warp] = before;
+  }
+  __syncthreads();
+  all = before = 0;
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
-          l += lw;
-          const int n = min(32, parts - i0);
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, wgt, i);
-            const float2 v = *(reinterpret_cast<const float2*>(p.ws_o + slot_of(i0 + i) * DH) + lane);
-            if (wi > 0.f) {
-              o0 += v.x * wi;
-              o1 += v.y * wi;
-            }
-          }
-        }
-        if (p.sinks != nullptr) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mmax);
+  for (int i = 0; i < 8; ++i) {
+    all += sum_all[i];
+    before += sum_before[i];
+  }
+  const long long per = share_of(all, p.parts, p.least);
+  const int c0 = static_cast<int>(before / per);
+  const int c1 = rows > 0 ? static_cast<int>((before + u.n - 1) / per) : c0;
+  const bool c0_first = before == per * c0;
+  const bool cut = c1 > c0;
+
+  const int block_rows = 1 << rows_log2, groups = 32 >> rows_log2;
+  const int x = threadIdx.x >> 3;             // row x group
+  const int grp = x >> rows_log2;
+  const int r = blockIdx.y * block_rows + (x & (block_rows - 1));
+  const int c8 = (threadIdx.x & 7) * 8;
+  float m = -INFINITY, l = 0.f;
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  if (cut && r < rows) {
+    for (int c = c0 + grp; c <= c1; c += groups) {
+      const int64_t cta = static_cast<int64_t>(c) * g.kv_heads + h;
+      const int64_t at = (2 * cta + (c == c0 && !c0_first ? 1 : 0)) * p.rows_cap + r;
+      const float2 ml = p.ws_ml[at];
+      const float4* src = reinterpret_cast<const float4*>(p.ws_o + at * DH + c8);
+      const float4 a = src[0], d = src[1];
+      if (ml.y != 0.f) {
+        const float m_new = fmaxf(m, ml.x);
+        const float keep = ex2_approx(m - m_new), wgt = ex2_approx(ml.x - m_new);
+        l = l * keep + ml.y * wgt;
+        o[0] = o[0] * keep + a.x * wgt;
+        o[1] = o[1] * keep + a.y * wgt;
+        o[2] = o[2] * keep + a.z * wgt;
+        o[3] = o[3] * keep + a.w * wgt;
+        o[4] = o[4] * keep + d.x * wgt;
+        o[5] = o[5] * keep + d.y * wgt;
+        o[6] = o[6] * keep + d.z * wgt;
+        o[7] = o[7] * keep + d.w * wgt;
+        m = m_new;
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    *(reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + head * DH) + lane) =
-        l > 0.f ? pack_half2(o0 * inv, o1 * inv) : 0u;
-    if (p.lse != nullptr && lane == 0) p.lse[row * g.n_heads + head] = l > 0.f ? mmax * kLn2 + logf(l) : -INFINITY;
   }
+  if (groups > 1) {
+    reinterpret_cast<float4*>(&sh_o[x][c8])[0] = make_float4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<float4*>(&sh_o[x][c8])[1] = make_float4(o[4], o[5], o[6], o[7]);
+    if (c8 == 0) sh_ml[x] = make_float2(m, l);
+    __syncthreads();
+    if (grp != 0) return;
+    float mx = -INFINITY;
+    for (int i = 0; i < groups; ++i) mx = fmaxf(mx, sh_ml[(i << rows_log2) + (x & (block_rows - 1))].x);
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = 0.f;
+    const int used = min(groups, c1 - c0 + 1);
+    if (mx != -INFINITY) {
+      for (int i = 0; i < used; ++i) {
+        const int y = (i << rows_log2) + (x & (block_rows - 1));
+        const float2 ml = sh_ml[y];
+        if (!(ml.y != 0.f)) continue;
+        const float wgt = ex2_approx(ml.x - mx);
+        l += ml.y * wgt;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += sh_o[y][c8 + j] * wgt;
+      }
+    }
+    m = mx;
+  }
+  if (r >= rows_out || (r < rows && !cut)) return;  // rows of whole units are written already
+  const int64_t row = static_cast<int64_t>(b) * g.t_q + u.tok0 + r / g.group;
+  const int head = h * g.group + r % g.group;
+  if (p.sinks != nullptr && l != 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - m);
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * DH + c8) =
+      make_uint4(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv),
+                 pack_half2(o[4] * inv, o[5] * inv), pack_half2(o[6] * inv, o[7] * inv));
+  if (p.lse != nullptr && c8 == 0) p.lse[row * g.n_heads + head] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
 }  // namespace pg

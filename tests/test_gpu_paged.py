@@ -391,3 +391,17 @@ def test_another_device_and_stream_are_refused_or_followed():
         attn.attn_paged(q, cache, 2, 1, 2)
     with pytest.raises(attn.AttnError):
         attn.attn_paged(q, cache, 1, 1, 2, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("t_q", [1, 12, 40])
+def test_nan_that_a_row_sees_comes_back_as_nan(t_q):
+    """A NaN key makes NaN of the rows that see it, and of no other sequence or head."""
+    rng = np.random.default_rng(16)
+    cache = make_cache(rng, [200, 90], 2, 16)
+    q = queries(rng, 2, t_q, 4)
+    clean, clean_lse = attn.attn_paged(q, cache, 2, t_q, 4, return_lse=True)
+    cache.k[int(cache.table[0, 3]) * 16 + 2, :64] = NAN
+    got, lse = attn.attn_paged(q, cache, 2, t_q, 4, return_lse=True)
+    assert torch.isnan(got[:t_q, :128]).all() and torch.isnan(lse[:t_q, :2]).all()
+    assert torch.equal(got[:t_q, 128:], clean[:t_q, 128:]) and torch.equal(got[t_q:], clean[t_q:])
+    assert torch.equal(lse[t_q:], clean_lse[t_q:])
