@@ -23,8 +23,8 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from dataclasses import dataclass
-from typing import Any, Optional
+from collections import namedtuple
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libattn.so")
@@ -191,9 +191,10 @@ def _mat(t, cols: Optional[int] = None) -> AttnMat:
         raise ValueError("expected a CUDA tensor (there is no CPU path)")
     if t.dtype != torch.float16:
         raise ValueError(f"expected float16, got {t.dtype}")
-    if t.dim() != 2 or t.stride(1) != 1:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError("expected a 2-D tensor with unit column stride")
-    return AttnMat(ctypes.c_void_p(t.data_ptr()), t.stride(0))
+    return AttnMat(t.data_ptr(), stride[0])
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -349,33 +350,44 @@ def encoder_layer_attention(x, w_qkv, b_q, b_v, batch, t, n_heads, mask_kind=MAS
 # paged K/V cache
 # ---------------------------------------------------------------------------
 
-@dataclass
-class PagedKV:
+class PagedKV(namedtuple("PagedKV", "k v table lens page_size n_kv_heads batch slots device c")):
     """A paged K/V cache: pools k and v [num_pages * page_size, n_kv_heads * 64]
     fp16 (column views of one buffer will do), table [batch, pages_per_seq] int32
     (entries outside [0, num_pages) are holes) and lens [batch] int32, the slots
     in use, new tokens included. Slot j of sequence b is row
-    table[b, j // page_size] * page_size + j % page_size."""
-    k: Any
-    v: Any
-    table: Any
-    lens: Any
-    page_size: int
-    n_kv_heads: int
+    table[b, j // page_size] * page_size + j % page_size.
 
-    @property
-    def slots(self) -> int:
-        """Slots per sequence that the table can address."""
-        return self.table.shape[1] * self.page_size
+    The tensors are checked here, once, and cannot be exchanged; what they hold
+    may change at any time (a captured graph follows table and lens). batch,
+    slots (per sequence), device and c (the C structure) follow from them."""
+    __slots__ = ()
+
+    def __new__(cls, k, v, table, lens, page_size: int, n_kv_heads: int):
+        import torch
+        if page_size not in (16, 32, 64, 128, 256):
+            raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {page_size}")
+        km, vm = _mat(k), _mat(v)
+        dev = k.device
+        (rows, k_cols), (v_rows, v_cols) = k.shape, v.shape
+        cols = n_kv_heads * HEAD_DIM
+        if v.device != dev or v_rows != rows:
+            raise ValueError("the K and V pools must lie on one device and have as many rows")
+        if rows == 0 or rows % page_size or n_kv_heads < 1 or k_cols < cols or v_cols < cols:
+            raise ValueError(f"the pools must hold whole pages of {page_size} rows of {cols} columns")
+        if table.dim() != 2:
+            raise ValueError("table must be a [batch, pages_per_seq] int32 tensor")
+        batch, per_seq = table.shape
+        c = AttnPagedKV(km, vm, _dev_tensor(table, "table", torch.int32, (batch, per_seq), dev),
+                        _dev_tensor(lens, "lens", torch.int32, (batch,), dev), rows // page_size, page_size, per_seq,
+                        n_kv_heads)
+        return tuple.__new__(cls, (k, v, table, lens, page_size, n_kv_heads, batch, per_seq * page_size, dev, c))
 
 
-def _dev_tensor(t, what: str, dtype, shape, device):
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor (there is no CPU path)")
+def _dev_tensor(t, what: str, dtype, shape, device) -> int:
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the cache on {device}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} tensor")
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {list(shape)} {dtype} tensor, got {list(t.shape)} {t.dtype}")
     return t.data_ptr()
 
 
@@ -383,52 +395,44 @@ def _rows(t, what: str, rows: int, cols: int, device) -> AttnMat:
     m = _mat(t)
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the cache on {device}")
-    if t.shape[0] != rows or t.shape[1] < cols:
-        raise ValueError(f"{what} must have {rows} rows of at least {cols} columns, got {list(t.shape)}")
+    have, wide = t.shape
+    if have != rows or wide < cols:
+        raise ValueError(f"{what} must have {rows} rows of at least {cols} columns, got [{have}, {wide}]")
     return m
 
 
-def _paged_kv(cache: PagedKV, batch: int) -> AttnPagedKV:
-    import torch
-    if cache.page_size not in (16, 32, 64, 128, 256):
-        raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {cache.page_size}")
-    k, v = _mat(cache.k), _mat(cache.v)
-    dev = cache.k.device
-    if cache.v.device != dev or cache.v.shape[0] != cache.k.shape[0]:
-        raise ValueError("the K and V pools must lie on one device and have as many rows")
-    rows, cols = cache.k.shape[0], cache.n_kv_heads * HEAD_DIM
-    if rows == 0 or rows % cache.page_size or min(cache.k.shape[1], cache.v.shape[1]) < cols:
-        raise ValueError(f"the pools must hold whole pages of {cache.page_size} rows of {cols} columns")
-    if cache.table.dim() != 2:
-        raise ValueError("table must be a [batch, pages_per_seq] int32 tensor")
-    table = _dev_tensor(cache.table, "table", torch.int32, (batch, cache.table.shape[1]), dev)
-    lens = _dev_tensor(cache.lens, "lens", torch.int32, (batch,), dev)
-    return AttnPagedKV(k, v, table, lens, rows // cache.page_size, cache.page_size, cache.table.shape[1],
-                       cache.n_kv_heads)
+def _batch_of(cache: PagedKV, batch: int) -> AttnPagedKV:
+    if batch != cache.batch:
+        raise ValueError(f"the cache holds {cache.batch} sequences, not {batch}")
+    return cache.c
 
 
-def _paged_mask(window, first, causal, q_lens, batch, device) -> AttnPagedMask:
+def _q_lens_ptr(q_lens, batch, device) -> int:
     import torch
-    ptr = 0 if q_lens is None else _dev_tensor(q_lens, "q_lens", torch.int32, (batch,), device)
-    return AttnPagedMask(window, first, 1 if causal else 0, ptr)
+    return 0 if q_lens is None else _dev_tensor(q_lens, "q_lens", torch.int32, (batch,), device)
 
 
 class _On:
     """The tensors' device and the call's stream as the current ones, so that
-    what is allocated and launched belongs to them."""
+    what is allocated and launched belongs to them. Entering yields the stream."""
+    __slots__ = ("ctx", "index")
 
     def __init__(self, device, stream):
         import torch
-        self.ctx = [torch.cuda.device(device)]
+        self.index = device.index
+        self.ctx = ()
+        if torch.cuda.current_device() != device.index:
+            self.ctx = (torch.cuda.device(device),)
         if stream is not None:
             if stream.device != device:
                 raise ValueError(f"the stream is on {stream.device}, the cache on {device}")
-            self.ctx.append(torch.cuda.stream(stream))
+            self.ctx += (torch.cuda.stream(stream),)
 
     def __enter__(self):
+        import torch
         for c in self.ctx:
             c.__enter__()
-        return _stream_ptr()
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
@@ -440,12 +444,12 @@ def attn_paged_append(k_new, v_new, cache: PagedKV, batch, t_new, q_lens=None, s
     views) into the slots at the end of each sequence; cache.lens already counts
     them, q_lens ([batch] int32) says how many of the t_new rows are valid."""
     lib = load_library()
-    kv = _paged_kv(cache, batch)
-    dev, cols = cache.k.device, cache.n_kv_heads * HEAD_DIM
+    kv = _batch_of(cache, batch)
+    dev, cols = cache.device, cache.n_kv_heads * HEAD_DIM
     kn, vn = _rows(k_new, "k_new", batch * t_new, cols, dev), _rows(v_new, "v_new", batch * t_new, cols, dev)
-    mask = _paged_mask(0, 0, True, q_lens, batch, dev)
+    lens = _q_lens_ptr(q_lens, batch, dev)
     with _On(dev, stream) as s:
-        _check(lib.attn_paged_append(kn, vn, kv, batch, t_new, mask.q_lens, s), "attn_paged_append")
+        _check(lib.attn_paged_append(kn, vn, kv, batch, t_new, lens, s), "attn_paged_append")
 
 
 def paged_workspace_size(batch, t_q, n_heads, n_kv_heads) -> int:
@@ -462,25 +466,33 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
     Without workspace one is allocated for the call."""
     import torch
     lib = load_library()
-    kv = _paged_kv(cache, batch)
-    dev, cols = cache.k.device, n_heads * HEAD_DIM
-    qm = _rows(q, "q", batch * t_q, cols, dev)
-    mask = _paged_mask(window, first, causal, q_lens, batch, dev)
+    kv = _batch_of(cache, batch)
+    dev, rows, cols = cache.device, batch * t_q, n_heads * HEAD_DIM
+    qm = _rows(q, "q", rows, cols, dev)
+    mask = AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, dev))
     sinks_ptr = 0 if sinks is None else _dev_tensor(sinks, "sinks", torch.float32, (n_heads,), dev)
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(batch * t_q, cols, dtype=torch.float16, device=dev)
-        if lse is None and return_lse:
-            lse = torch.empty(batch * t_q, n_heads, dtype=torch.float32, device=dev)
-        lse_ptr = 0 if lse is None else _dev_tensor(lse, "lse", torch.float32, (batch * t_q, n_heads), dev)
+            out = q.new_empty((rows, cols))
+            om = AttnMat(out.data_ptr(), cols)
+        else:
+            om = _rows(out, "out", rows, cols, dev)
+        if lse is not None:
+            lse_ptr = _dev_tensor(lse, "lse", torch.float32, (rows, n_heads), dev)
+        elif return_lse:
+            lse = q.new_empty((rows, n_heads), dtype=torch.float32)
+            lse_ptr = lse.data_ptr()
+        else:
+            lse_ptr = 0
         if workspace is None:
-            workspace = torch.empty(max(16, paged_workspace_size(batch, t_q, n_heads, cache.n_kv_heads)),
-                                    dtype=torch.uint8, device=dev)
-        elif workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, the cache on {dev}")
-        st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, float(scale),
-                            _rows(out, "out", batch * t_q, cols, dev), lse_ptr, _ptr(workspace),
-                            workspace.numel() * workspace.element_size(), s)
+            ws_bytes = lib.attn_paged_workspace_size(batch, t_q, n_heads, cache.n_kv_heads)
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+        else:
+            if workspace.device != dev:
+                raise ValueError(f"workspace is on {workspace.device}, the cache on {dev}")
+            ws_bytes = workspace.numel() * workspace.element_size()
+        st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, scale, om, lse_ptr,
+                            workspace.data_ptr(), ws_bytes, s)
         _check(st, "attn_paged")
     return out if lse is None else (out, lse)
 
@@ -492,18 +504,18 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
     Returns out, a new tensor unless given; out=weights adds in place."""
     import torch
     lib = load_library()
-    kv = _paged_kv(cache, batch)
-    dev = cache.k.device
-    qm = _rows(q, "q", batch * t_q, n_heads * HEAD_DIM, dev)
-    mask = _paged_mask(window, first, causal, q_lens, batch, dev)
-    lse_ptr = _dev_tensor(lse, "lse", torch.float32, (batch * t_q, n_heads), dev)
+    kv = _batch_of(cache, batch)
+    dev, rows = cache.device, batch * t_q
+    qm = _rows(q, "q", rows, n_heads * HEAD_DIM, dev)
+    mask = AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, dev))
+    lse_ptr = _dev_tensor(lse, "lse", torch.float32, (rows, n_heads), dev)
     shape = (batch, cache.slots)
     w_in = 0 if weights is None else _dev_tensor(weights, "weights", torch.float32, shape, dev)
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=dev)
+            out = lse.new_empty(shape)
         w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
-        st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, float(scale), w_in, w_out, s)
+        st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out, s)
         _check(st, "attn_paged_weights")
     return out
 
@@ -519,21 +531,19 @@ def attn_paged_evict(cache: PagedKV, weights, budget, first=0, recent=0, dst: Op
     weights_out=weights works in place when dst has as many slots."""
     import torch
     lib = load_library()
-    batch = cache.table.shape[0]
-    kv = _paged_kv(cache, batch)
-    dev = cache.k.device
+    batch, dev = cache.batch, cache.device
     if dst is None:
         dst = cache
-    if dst.k.device != dev:
-        raise ValueError(f"dst is on {dst.k.device}, the cache on {dev}")
-    to = _paged_kv(dst, batch)
+    if dst.device != dev:
+        raise ValueError(f"dst is on {dst.device}, the cache on {dev}")
+    to = _batch_of(dst, batch)
     w_in = _dev_tensor(weights, "weights", torch.float32, (batch, cache.slots), dev)
     with _On(dev, stream) as s:
         if kept is None:
-            kept = torch.empty(batch, budget, dtype=torch.int32, device=dev)
+            kept = weights.new_empty((batch, budget), dtype=torch.int32)
         if weights_out is None:
-            weights_out = torch.empty(batch, dst.slots, dtype=torch.float32, device=dev)
-        st = lib.attn_paged_evict(kv, batch, budget, first, recent, w_in, to,
+            weights_out = weights.new_empty((batch, dst.slots))
+        st = lib.attn_paged_evict(cache.c, batch, budget, first, recent, w_in, to,
                                   _dev_tensor(weights_out, "weights_out", torch.float32, (batch, dst.slots), dev),
                                   _dev_tensor(kept, "kept", torch.int32, (batch, budget), dev), s)
         _check(st, "attn_paged_evict")

@@ -115,19 +115,13 @@ def test_workspace_size_of_invalid_sizes_is_zero(lib):
     assert lib.attn_paged_workspace_size(1, 1, 129, 1) == 0
 
 
-def test_binding_refuses_tensors_off_the_gpu():
-    kv = attn.PagedKV(torch.zeros(32, 128, dtype=torch.float16), torch.zeros(32, 128, dtype=torch.float16),
-                      torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), 16, 2)
-    q = torch.zeros(1, 128, dtype=torch.float16)
-    with pytest.raises(ValueError):
-        attn.attn_paged(q, kv, 1, 1, 2)
-    with pytest.raises(ValueError):
-        attn.attn_paged_append(q, q, kv, 1, 1)
-    with pytest.raises(ValueError):
-        attn.attn_paged_evict(kv, torch.zeros(1, 32), 8)
-    kv.page_size = 24
+def test_binding_refuses_bad_caches():
+    k = torch.zeros(32, 128, dtype=torch.float16)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        attn.PagedKV(k, k, table, lens, 16, 2)
     with pytest.raises(ValueError, match="page_size"):
-        attn.attn_paged(q, kv, 1, 1, 2)
+        attn.PagedKV(k, k, table, lens, 24, 2)
 
 
 # ---------------------------------------------------------------------------
