@@ -6,9 +6,9 @@
 // Evict: of the slots that hold something, keep the `first` first, the
 // `recent` last and the heaviest of the rest up to `budget`, ties to the
 // lowest slot, and move what is kept, in order, to the front.
-//   select  one CTA per sequence: the weights as 32-bit keys that order like
-//           them, a radix selection of the budget-th largest key (four passes
-//           of 8 bits over the keys), then a scan that numbers the kept slots.
+//   select  the weights as 32-bit keys that order like them, a radix selection
+//           of the budget-th largest key (up to four passes of 8 bits), then a
+//           scan that numbers the kept slots.
 //   move    bound by the bytes moved. Kept slot n comes from slot kept[n] >= n,
 //           so a CTA that owns some columns of a sequence and walks the rows
 //           upwards, loading a step before it stores it, may work in place.
@@ -66,6 +66,7 @@ struct EvictParams {
   __half *k_out, *v_out;
   int64_t k_out_stride, v_out_stride;
   int rows_per_cta;       // move: rows of a CTA (budget when in place)
+  int move_vecs;          // and 16-byte pieces of a row
 };
 
 // Keys that order like the weights: 0 for a slot that holds nothing, all ones
@@ -80,107 +81,159 @@ __device__ __forceinline__ uint32_t evict_key(const EvictParams& p, const Seq& s
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// Select: a cluster of up to 8 CTAs per sequence, each with an equal run of its
+// slots. Bound by latency: a pass costs a histogram in shared memory, a cluster
+// barrier and 8 remote reads per digit, so the keys are computed once (8192 of
+// a CTA's stay in shared memory; longer runs recompute the rest).
 constexpr int SELECT_THREADS = 1024;
+constexpr int SELECT_CACHED = 8192;
+
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(const uint32_t* mine, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(mine), rank)) : "memory");
+  return v;
+}
 
 __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const EvictParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t found[2];              // digit, how many are still wanted
-  __shared__ uint32_t warp_gt[32], warp_eq[32];
+  __shared__ uint32_t keys[SELECT_CACHED];
+  __shared__ uint32_t hist[2][256];          // by pass, so one cluster barrier per pass is enough
+  __shared__ uint32_t warp_sum[32], warp_eq[32];
+  __shared__ uint32_t found[3];              // digit, how many of it are wanted, how many there are
+  __shared__ uint32_t counts[2];             // this CTA's larger and equal keys
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int rank = blockIdx.x, ranks = gridDim.x, b = blockIdx.y;
+  if (t < 512) hist[t >> 8][t & 255] = 0u;
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.x;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const Seq s = seq_of(p.g, b);
   const float* w = p.w_in + static_cast<int64_t>(b) * p.g.cap;
-  // The budget-th largest key: prefix, digit by digit from the top.
-  uint32_t prefix = 0, want = static_cast<uint32_t>(p.budget);
-  bool all = false;  // fewer slots than the budget
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (t < 256) hist[t] = 0u;
-    __syncthreads();
-    for (int j0 = 0; j0 < s.kv; j0 += SELECT_THREADS) {
+  const int run = (s.kv + ranks - 1) / ranks;
+  const int ja = min(s.kv, rank * run), jz = min(s.kv, ja + run);
+  auto key_at = [&](int j) { return j - ja < SELECT_CACHED ? keys[j - ja] : evict_key(p, s, b, j, w); };
+  for (int j = ja + t; j < min(jz, ja + SELECT_CACHED); j += SELECT_THREADS) keys[j - ja] = evict_key(p, s, b, j, w);
+  __syncthreads();
+
+  // The budget-th largest key, digit by digit from the top: kept are the keys
+  // of at least `limit` (and then no equal ones), or those above it and the
+  // first `want` equal ones.
+  uint32_t prefix = 0, limit = 1, want = static_cast<uint32_t>(p.budget);
+  bool equal = false;  // `limit` is one key's value and only `want` of it stay
+  for (int pass = 0; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+    uint32_t* h = hist[pass & 1];
+    for (int j0 = ja; j0 < jz; j0 += SELECT_THREADS) {
       const int j = j0 + t;
-      const uint32_t key = j < s.kv ? evict_key(p, s, b, j, w) : 0u;
-      const bool in = key != 0u && (shift == 24 || (key >> (shift + 8)) == prefix);
-      // equal digits of a warp count once
+      const uint32_t key = j < jz ? key_at(j) : 0u;
+      const bool in = key != 0u && (pass == 0 || (key >> (shift + 8)) == prefix);
       const uint32_t digit = in ? (key >> shift) & 255u : 256u;
-      const uint32_t same = __match_any_sync(0xffffffffu, digit);
-      if (in && lane == __ffs(same) - 1) atomicAdd(&hist[digit], __popc(same));
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);  // equal digits of a warp count once
+      if (in && lane == __ffs(same) - 1) atomicAdd(&h[digit], __popc(same));
     }
-    __syncthreads();
-    if (warp == 0) {
-      // lane i holds digits [8i, 8i + 8); digits above come first
-      uint32_t mine = 0;
-      for (int i = 0; i < 8; ++i) mine += hist[8 * lane + i];
-      uint32_t above = 0;  // keys in higher lanes
-      for (int o = 31; o > 0; --o) {
-        const uint32_t x = __shfl_sync(0xffffffffu, mine, o);
-        if (lane < o) above += x;
+    cluster_sync();
+    uint32_t mine = 0, above = 0;
+    if (t < 256) {
+      for (int r = 0; r < ranks; ++r) mine += ld_shared_cluster_u32(&h[255 - t], r);  // thread t: digit 255 - t
+      uint32_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
       }
-      if (shift == 24 && lane == 0) found[1] = 0xFFFFFFFFu;
-      __syncwarp();
+      if (lane == 31) warp_sum[warp] = incl;
+      above = incl - mine;
+    }
+    if (t == 0) found[2] = 0u;
+    __syncthreads();
+    if (t < 256) {
+      for (int i = 0; i < warp; ++i) above += warp_sum[i];
       if (above < want && above + mine >= want) {
-        uint32_t left = want - above;
-        int d = 8 * lane + 7;
-        while (hist[d] < left) left -= hist[d--];
-        found[0] = d;
-        found[1] = left;
+        found[0] = 255 - t;
+        found[1] = want - above;
+        found[2] = mine;
       }
+      hist[(pass + 1) & 1][t] = 0u;  // read by others before the last barrier
     }
     __syncthreads();
-    if (shift == 24 && found[1] == 0xFFFFFFFFu) {
-      all = true;
-      break;
-    }
+    if (found[2] == 0u) break;  // fewer slots than the budget: all stay
     prefix = prefix << 8 | found[0];
     want = found[1];
-    __syncthreads();
+    limit = prefix << shift;
+    if (found[2] == want) break;  // every key of this digit stays
+    equal = pass == 3;
   }
-  // Number the kept slots in order: larger keys, and the first `want` equal ones.
-  uint32_t base_gt = 0, base_eq = 0;
+  auto larger = [&](uint32_t key) { return key != 0u && (equal ? key > limit : key >= limit); };
+
+  // Number what stays, in order. Earlier CTAs' counts first.
+  uint32_t n_gt = 0, n_eq = 0;
+  for (int j = ja + t; j < jz; j += SELECT_THREADS) {
+    const uint32_t key = key_at(j);
+    n_gt += larger(key);
+    n_eq += equal && key == limit;
+  }
+  n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+  n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+  if (lane == 0) {
+    warp_sum[warp] = n_gt;
+    warp_eq[warp] = n_eq;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    counts[0] = __reduce_add_sync(0xffffffffu, warp_sum[lane]);
+    counts[1] = __reduce_add_sync(0xffffffffu, warp_eq[lane]);
+  }
+  cluster_sync();
+  uint32_t base_gt = 0, base_eq = 0, total = 0, total_eq = 0;
+  for (int r = 0; r < ranks; ++r) {
+    const uint32_t x = ld_shared_cluster_u32(&counts[0], r), y = ld_shared_cluster_u32(&counts[1], r);
+    if (r < rank) {
+      base_gt += x;
+      base_eq += y;
+    }
+    total += x;
+    total_eq += y;
+  }
+  const int count = static_cast<int>(total + min(total_eq, equal ? want : 0u));
   int* kept = p.kept + static_cast<int64_t>(b) * p.budget;
-  float* w_out = p.w_out != nullptr ? p.w_out + static_cast<int64_t>(b) * p.out_cap : nullptr;
-  for (int j0 = 0; j0 < s.kv; j0 += SELECT_THREADS) {
+  for (int j0 = ja; j0 < jz; j0 += SELECT_THREADS) {
     const int j = j0 + t;
-    const uint32_t key = j < s.kv ? evict_key(p, s, b, j, w) : 0u;
-    const float wj = j < s.kv ? w[j] : 0.f;
-    const bool gt = all ? key != 0u : key > prefix;
-    const bool eq = !all && key == prefix && key != 0u;
+    const uint32_t key = j < jz ? key_at(j) : 0u;
+    const bool gt = larger(key), eq = equal && key == limit;
     const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    __syncthreads();
     if (lane == 0) {
-      warp_gt[warp] = __popc(bg);
+      warp_sum[warp] = __popc(bg);
       warp_eq[warp] = __popc(be);
     }
     __syncthreads();
-    uint32_t g_before = base_gt, e_before = base_eq, g_all = 0, e_all = 0;
-    {
-      const uint32_t xg = warp_gt[lane], xe = warp_eq[lane];
-      g_all = __reduce_add_sync(0xffffffffu, xg);
-      e_all = __reduce_add_sync(0xffffffffu, xe);
-      g_before += __reduce_add_sync(0xffffffffu, lane < warp ? xg : 0u);
-      e_before += __reduce_add_sync(0xffffffffu, lane < warp ? xe : 0u);
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    g_before += __popc(bg & below);
-    e_before += __popc(be & below);
-    if (gt || (eq && e_before < want)) {
-      const uint32_t n = g_before + min(e_before, want);
-      kept[n] = j;
-      if (w_out != nullptr) w_out[n] = wj;  // n <= j: these weights have been read
-    }
-    base_gt += g_all;
-    base_eq += e_all;
-    __syncthreads();
+    const uint32_t xg = warp_sum[lane], xe = warp_eq[lane], below = (1u << lane) - 1u;
+    const uint32_t g_before = base_gt + __reduce_add_sync(0xffffffffu, lane < warp ? xg : 0u) + __popc(bg & below);
+    const uint32_t e_before = base_eq + __reduce_add_sync(0xffffffffu, lane < warp ? xe : 0u) + __popc(be & below);
+    if (gt || (eq && e_before < want)) kept[g_before + min(e_before, want)] = j;
+    base_gt += __reduce_add_sync(0xffffffffu, xg);
+    base_eq += __reduce_add_sync(0xffffffffu, xe);
   }
-  const int count = static_cast<int>(all ? base_gt : p.budget);
-  for (int n = count + t; n < p.budget; n += SELECT_THREADS) kept[n] = -1;
-  if (w_out != nullptr)
-    for (int n = count + t; n < p.out_cap; n += SELECT_THREADS) w_out[n] = 0.f;
-  if (t == 0) p.out_lens[b] = count;
+  for (int n = count + rank * SELECT_THREADS + t; n < p.budget; n += ranks * SELECT_THREADS) kept[n] = -1;
+
+  // The weights move like the rows: n <= kept[n], so with a barrier between the
+  // reads and the writes of a step w_out may be w_in.
+  __threadfence();  // kept, for the other CTAs
+  cluster_sync();
+  if (p.w_out != nullptr) {
+    float* w_out = p.w_out + static_cast<int64_t>(b) * p.out_cap;
+    for (int n0 = 0; n0 < count; n0 += ranks * SELECT_THREADS) {
+      const int n = n0 + rank * SELECT_THREADS + t;
+      float x = 0.f;
+      if (n < count) x = w[*const_cast<const volatile int*>(kept + n)];
+      cluster_sync();
+      if (n < count) w_out[n] = x;
+    }
+    for (int n = count + rank * SELECT_THREADS + t; n < p.out_cap; n += ranks * SELECT_THREADS) w_out[n] = 0.f;
+  }
+  if (rank == 0 && t == 0) p.out_lens[b] = count;
 }
 
-// Rows of the kept slots: CTA (row range, K or V head, sequence), 8 threads
-// per 128-byte head row.
+// Moves the rows of the kept slots: CTA (row range, columns of K or of V,
+// sequence), a step of MOVE_STEPS 16-byte pieces per thread, row by row.
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_STEPS = 4;
 
@@ -188,38 +241,41 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_move_kernel(const EvictPar
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.z;
-  const int heads = gridDim.y / 2;
-  const bool is_v = static_cast<int>(blockIdx.y) >= heads;
-  const int col = (is_v ? blockIdx.y - heads : blockIdx.y) * DH + (threadIdx.x & 7) * 8;
-  const __half* src = (is_v ? p.v : p.k) + col;
-  __half* dst = (is_v ? p.v_out : p.k_out) + col;
-  const int64_t ss = is_v ? p.v_stride : p.k_stride, ds = is_v ? p.v_out_stride : p.k_out_stride;
+  const int halves = gridDim.y / 2;  // column ranges of K, then of V
+  const bool is_v = static_cast<int>(blockIdx.y) >= halves;
+  const int col0 = (is_v ? blockIdx.y - halves : blockIdx.y) * p.move_vecs;
+  const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v : p.k) + col0;
+  uint4* dst = reinterpret_cast<uint4*>(is_v ? p.v_out : p.k_out) + col0;
+  const int64_t ss = (is_v ? p.v_stride : p.k_stride) / 8, ds = (is_v ? p.v_out_stride : p.k_out_stride) / 8;
   const int mask = (1 << p.g.page_shift) - 1;
-  const int n_end = min(p.budget, static_cast<int>(blockIdx.x + 1) * p.rows_per_cta);
+  const int n_begin = blockIdx.x * p.rows_per_cta;
+  const int n_end = min(p.budget, n_begin + p.rows_per_cta);
   const int* kept = p.kept + static_cast<int64_t>(b) * p.budget;
   const int* t_in = p.g.table + static_cast<int64_t>(b) * p.g.pages_per_seq;
   const int* t_out = p.out_table + static_cast<int64_t>(b) * p.out_pages_per_seq;
-  constexpr int ROWS = MOVE_THREADS / 8;
-  for (int n0 = blockIdx.x * p.rows_per_cta; n0 < n_end; n0 += ROWS * MOVE_STEPS) {
+  const int64_t pieces = static_cast<int64_t>(n_end - n_begin) * p.move_vecs;
+  for (int64_t x0 = 0; x0 < pieces; x0 += MOVE_THREADS * MOVE_STEPS) {
     uint4 x[MOVE_STEPS];
     int64_t to[MOVE_STEPS];
 #pragma unroll
     for (int i = 0; i < MOVE_STEPS; ++i) {
-      const int n = n0 + i * ROWS + static_cast<int>(threadIdx.x >> 3);
+      const int64_t at = x0 + i * MOVE_THREADS + threadIdx.x;
       to[i] = -1;
-      if (n >= n_end) continue;
+      if (at >= pieces) continue;
+      const int row = static_cast<int>(at / p.move_vecs);
+      const int vec = static_cast<int>(at - static_cast<int64_t>(row) * p.move_vecs);
+      const int n = n_begin + row;
       const int j = kept[n];
       if (j < 0) continue;
       const int pi = t_in[j >> p.g.page_shift], po = t_out[n >> p.g.page_shift];
       if (po < 0 || po >= p.out_num_pages) continue;
-      const int64_t from = (static_cast<int64_t>(pi) << p.g.page_shift) + (j & mask);
-      to[i] = (static_cast<int64_t>(po) << p.g.page_shift) + (n & mask);
-      x[i] = *reinterpret_cast<const uint4*>(src + from * ss);
+      to[i] = ((static_cast<int64_t>(po) << p.g.page_shift) + (n & mask)) * ds + vec;
+      x[i] = src[((static_cast<int64_t>(pi) << p.g.page_shift) + (j & mask)) * ss + vec];
     }
     __syncthreads();  // this step's rows are read before any is overwritten
 #pragma unroll
     for (int i = 0; i < MOVE_STEPS; ++i)
-      if (to[i] >= 0) *reinterpret_cast<uint4*>(dst + to[i] * ds) = x[i];
+      if (to[i] >= 0) dst[to[i]] = x[i];
   }
 }
 

@@ -335,12 +335,17 @@ attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budge
   p.v_out = static_cast<__half*>(dst.v.ptr);
   p.k_out_stride = dst.k.row_stride;
   p.v_out_stride = dst.v.row_stride;
-  if (launch_pdl(sea::pg::paged_select_kernel, dim3(batch), dim3(sea::pg::SELECT_THREADS), 0, stream, p) != cudaSuccess)
+  int ranks = 1;
+  while (ranks < 8 && static_cast<int64_t>(ranks) * sea::pg::SELECT_THREADS < cap) ranks *= 2;
+  if (launch_pdl_cluster(sea::pg::paged_select_kernel, dim3(ranks, batch), dim3(sea::pg::SELECT_THREADS), 0, stream,
+                         static_cast<unsigned>(ranks), p) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  // Other pools: rows in any order. The same pool: each CTA walks all rows upwards.
-  constexpr int kStep = sea::pg::MOVE_THREADS / 8 * sea::pg::MOVE_STEPS;
-  p.rows_per_cta = same ? budget : kStep;
-  const dim3 grid(ceil_div(budget, p.rows_per_cta), 2 * cache.n_kv_heads, batch);
+  // Other pools: CTAs of 8 whole rows, in any order, so that a row's bytes are
+  // read together. The same pool: a CTA per head's columns, which walks all rows.
+  const int row_vecs = cache.n_kv_heads * sea::pg::DH / 8;
+  p.rows_per_cta = same ? budget : 8;
+  p.move_vecs = same ? sea::pg::DH / 8 : row_vecs;
+  const dim3 grid(ceil_div(budget, p.rows_per_cta), 2 * (row_vecs / p.move_vecs), batch);
   if (launch_pdl(sea::pg::paged_move_kernel, grid, dim3(sea::pg::MOVE_THREADS), 0, stream, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
