@@ -14,6 +14,7 @@
 //           upwards, loading a step before it stores it, may work in place.
 #pragma once
 
+#include "flash_attn.cuh"
 #include "paged_common.cuh"
 
 namespace sea {
@@ -25,20 +26,23 @@ struct AppendParams {
   int64_t k_new_stride, v_new_stride;
   __half *k, *v;
   int64_t k_stride, v_stride;
-  int vecs;  // 16-byte pieces per row
+  int vecs;            // 16-byte pieces per row
+  int rows_per_cta;
+  fa::DivC dv_vecs, dv_t;
 };
 
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const Geo& g = p.g;
-  const int64_t total = static_cast<int64_t>(g.batch) * g.t_q * p.vecs;
-  for (int64_t x = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; x < total;
-       x += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t row = x / p.vecs;
-    const int v = static_cast<int>(x - row * p.vecs);
-    const int b = static_cast<int>(row / g.t_q);
-    const int i = static_cast<int>(row - static_cast<int64_t>(b) * g.t_q);
+  const int row0 = blockIdx.x * p.rows_per_cta;
+  const int pieces = min(p.rows_per_cta, g.batch * g.t_q - row0) * p.vecs;
+  for (int x = threadIdx.x; x < pieces; x += 256) {
+    const int local = fa::div_c(x, p.dv_vecs);
+    const int v = x - local * p.vecs;
+    const int row = row0 + local;
+    const int b = fa::div_c(row, p.dv_t);
+    const int i = row - b * g.t_q;
     const Seq s = seq_of(g, b);
     const int slot = i + s.off;
     if (i >= s.q || slot < 0) continue;
@@ -67,6 +71,7 @@ struct EvictParams {
   int64_t k_out_stride, v_out_stride;
   int rows_per_cta;       // move: rows of a CTA (budget when in place)
   int move_vecs;          // and 16-byte pieces of a row
+  fa::DivC dv_vecs;
 };
 
 // Keys that order like the weights: 0 for a slot that holds nothing, all ones
@@ -253,17 +258,17 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_move_kernel(const EvictPar
   const int* kept = p.kept + static_cast<int64_t>(b) * p.budget;
   const int* t_in = p.g.table + static_cast<int64_t>(b) * p.g.pages_per_seq;
   const int* t_out = p.out_table + static_cast<int64_t>(b) * p.out_pages_per_seq;
-  const int64_t pieces = static_cast<int64_t>(n_end - n_begin) * p.move_vecs;
-  for (int64_t x0 = 0; x0 < pieces; x0 += MOVE_THREADS * MOVE_STEPS) {
+  const int pieces = (n_end - n_begin) * p.move_vecs;  // below 2^23 * 8, or a few rows
+  for (int x0 = 0; x0 < pieces; x0 += MOVE_THREADS * MOVE_STEPS) {
     uint4 x[MOVE_STEPS];
     int64_t to[MOVE_STEPS];
 #pragma unroll
     for (int i = 0; i < MOVE_STEPS; ++i) {
-      const int64_t at = x0 + i * MOVE_THREADS + threadIdx.x;
+      const int at = x0 + i * MOVE_THREADS + static_cast<int>(threadIdx.x);
       to[i] = -1;
       if (at >= pieces) continue;
-      const int row = static_cast<int>(at / p.move_vecs);
-      const int vec = static_cast<int>(at - static_cast<int64_t>(row) * p.move_vecs);
+      const int row = fa::div_c(at, p.dv_vecs);
+      const int vec = at - row * p.move_vecs;
       const int n = n_begin + row;
       const int j = kept[n];
       if (j < 0) continue;

@@ -152,8 +152,10 @@ attn_status launch_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv ca
   p.k_stride = cache.k.row_stride;
   p.v_stride = cache.v.row_stride;
   p.vecs = static_cast<int>(cols / 8);
-  const int64_t blocks = (rows * p.vecs + 255) / 256;
-  const int grid = static_cast<int>(std::min<int64_t>(blocks, int64_t(16) * dev->num_sms));
+  p.rows_per_cta = std::max(1, 512 / p.vecs);
+  p.dv_vecs = make_divc(p.vecs);
+  p.dv_t = make_divc(t_new);
+  const int grid = ceil_div(rows, p.rows_per_cta);
   if (launch_pdl(sea::pg::paged_append_kernel, dim3(grid), dim3(256), 0, stream, p) != cudaSuccess) return ATTN_ERR_CUDA;
   return ATTN_OK;
 }
@@ -340,11 +342,13 @@ attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budge
   if (launch_pdl_cluster(sea::pg::paged_select_kernel, dim3(ranks, batch), dim3(sea::pg::SELECT_THREADS), 0, stream,
                          static_cast<unsigned>(ranks), p) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  // Other pools: CTAs of 8 whole rows, in any order, so that a row's bytes are
-  // read together. The same pool: a CTA per head's columns, which walks all rows.
+  // Other pools: CTAs of a few whole rows, one step each, in any order, so that
+  // a row's bytes are read together. The same pool: a CTA per head's columns,
+  // which walks all rows.
   const int row_vecs = cache.n_kv_heads * sea::pg::DH / 8;
-  p.rows_per_cta = same ? budget : 8;
+  p.rows_per_cta = same ? budget : std::max(1, sea::pg::MOVE_THREADS * sea::pg::MOVE_STEPS / row_vecs);
   p.move_vecs = same ? sea::pg::DH / 8 : row_vecs;
+  p.dv_vecs = make_divc(p.move_vecs);
   const dim3 grid(ceil_div(budget, p.rows_per_cta), 2 * (row_vecs / p.move_vecs), batch);
   if (launch_pdl(sea::pg::paged_move_kernel, grid, dim3(sea::pg::MOVE_THREADS), 0, stream, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
