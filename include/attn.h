@@ -327,7 +327,8 @@ attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t
                        attn_paged_mask mask, const float *sinks, float scale, attn_mat out, float *lse,
                        void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
-/* Bytes of workspace attn_paged needs for these sizes on the current device (0 for invalid sizes). */
+/* Bytes of workspace attn_paged and attn_paged_weights need for these sizes on the current device (0 for
+   invalid sizes). */
 size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, int32_t n_kv_heads);
 
 /*
@@ -338,10 +339,11 @@ size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, in
  *   lse    [batch*t_q, n_heads] fp32
  *   w_in   [batch, pages_per_seq*page_size] fp32, or NULL for zeros
  *   w_out  the same shape; w_in itself, or not overlapping it
+ * workspace: as for attn_paged.
  */
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                attn_paged_mask mask, const float *lse, float scale, const float *w_in, float *w_out,
-                               attn_stream_t stream);
+                               void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /*
  * attn_paged_evict -- shrinks each sequence to at most `budget` slots

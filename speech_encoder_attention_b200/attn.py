@@ -130,7 +130,7 @@ SIGNATURES = {
     "attn_paged_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 4),
     "attn_paged_weights": (ctypes.c_int, [AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                           AttnPagedMask, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
-                                          ctypes.c_void_p, ctypes.c_void_p]),
+                                          ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "attn_paged_evict": (ctypes.c_int, [AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                         ctypes.c_void_p, AttnPagedKV, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p]),
@@ -456,6 +456,16 @@ def paged_workspace_size(batch, t_q, n_heads, n_kv_heads) -> int:
     return int(load_library().attn_paged_workspace_size(batch, t_q, n_heads, n_kv_heads))
 
 
+def _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads):
+    if workspace is None:
+        import torch
+        nbytes = lib.attn_paged_workspace_size(batch, t_q, n_heads, cache.n_kv_heads)
+        return q.new_empty(nbytes, dtype=torch.uint8), nbytes
+    if workspace.device != cache.device:
+        raise ValueError(f"workspace is on {workspace.device}, the cache on {cache.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal=True, q_lens=None, sinks=None,
                scale=DEFAULT_SCALE, out=None, return_lse=False, lse=None, workspace=None, stream=None):
     """Attention of a chunk of new tokens (t_q = 1: a decode step) over a paged
@@ -484,13 +494,7 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
             lse_ptr = lse.data_ptr()
         else:
             lse_ptr = 0
-        if workspace is None:
-            ws_bytes = lib.attn_paged_workspace_size(batch, t_q, n_heads, cache.n_kv_heads)
-            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
-        else:
-            if workspace.device != dev:
-                raise ValueError(f"workspace is on {workspace.device}, the cache on {dev}")
-            ws_bytes = workspace.numel() * workspace.element_size()
+        workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
         st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, scale, om, lse_ptr,
                             workspace.data_ptr(), ws_bytes, s)
         _check(st, "attn_paged")
@@ -498,10 +502,11 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
 
 
 def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, first=0, causal=True, q_lens=None,
-                       scale=DEFAULT_SCALE, weights=None, out=None, stream=None):
+                       scale=DEFAULT_SCALE, weights=None, out=None, workspace=None, stream=None):
     """What attn_paged's rows put on each slot, summed over rows and heads, added
     to weights ([batch, cache.slots] fp32; None: zeros). lse is attn_paged's.
-    Returns out, a new tensor unless given; out=weights adds in place."""
+    Returns out, a new tensor unless given; out=weights adds in place. workspace
+    as for attn_paged."""
     import torch
     lib = load_library()
     kv = _batch_of(cache, batch)
@@ -515,7 +520,9 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
         if out is None:
             out = lse.new_empty(shape)
         w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
-        st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out, s)
+        workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
+        st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out,
+                                    workspace.data_ptr(), ws_bytes, s)
         _check(st, "attn_paged_weights")
     return out
 

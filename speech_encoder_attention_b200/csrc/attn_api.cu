@@ -703,8 +703,9 @@ size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, in
 
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
-                               attn_stream_t stream) {
-  return launch_paged_weights(q, cache, batch, t_q, n_heads, mask, lse, scale, w_in, w_out, stream);
+                               void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  return launch_paged_weights(q, cache, batch, t_q, n_heads, mask, lse, scale, w_in, w_out, workspace,
+                              workspace_bytes, stream);
 }
 
 attn_status attn_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,

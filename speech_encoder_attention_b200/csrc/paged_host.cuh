@@ -236,7 +236,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
 
 attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                  attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
-                                 cudaStream_t stream) {
+                                 void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch) ||
       !valid_paged_mask(mask))
     return ATTN_ERR_INVALID;
@@ -251,6 +251,7 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   if (overlaps(rw, mat_range(q.ptr, rows, cols, q.row_stride)) || overlaps(rw, byte_range(lse, 4 * rows * n_heads)) ||
       overlaps(rw, pool_range(cache, cache.k)))
     return ATTN_ERR_INVALID;
+  if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_INVALID;
 
   DeviceInfo* dev = nullptr;
   if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
@@ -260,6 +261,7 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   // Rows of a query tile: as few as hold the chunk, a whole number of tokens.
   const int n = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : 128;
   p.g.tok_per_tile = static_cast<int>(std::min<int64_t>(t_q, n / p.g.group));
+  p.dv_group = make_divc(p.g.group);
   p.lse = lse;
   p.w_in = w_in;
   p.w_out = w_out;
@@ -269,23 +271,25 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   CUtensorMap tq, tk;
   if (!encode_paged_q(&tq, q, batch, t_q, n_heads, p.g.group, p.g.tok_per_tile) || !encode_pages(&tk, cache, cache.k))
     return ATTN_ERR_CUDA;
-  const int tiles = ceil_div(p.g.cap, sea::pg::BKV);
-  // Ranks of a key tile's cluster: enough CTAs for about three per SM, as long
-  // as every rank has an item.
-  const int64_t items = static_cast<int64_t>(cache.n_kv_heads) * ceil_div(t_q, p.g.tok_per_tile);
-  if (items > INT32_MAX / 8) return ATTN_ERR_INVALID;
-  int ranks = 1;
-  while (ranks < 8 && 2 * ranks <= items && static_cast<int64_t>(tiles) * batch * ranks < 3 * dev->num_sms) ranks *= 2;
-  const dim3 grid(ranks, batch, tiles);
-  auto launch = [&](auto kernel, int threads, int smem) {
-    return launch_pdl_cluster(kernel, grid, dim3(threads), smem, stream, static_cast<unsigned>(ranks), tq, tk, p);
+  p.tiles = ceil_div(p.g.cap, sea::pg::BKV);
+  if (static_cast<int64_t>(batch) * p.tiles > INT32_MAX ||
+      static_cast<int64_t>(cache.n_kv_heads) * ceil_div(t_q, p.g.tok_per_tile) > INT32_MAX)
+    return ATTN_ERR_INVALID;
+  auto launch = [&](auto kernel, auto cfg) -> attn_status {
+    using C = decltype(cfg);
+    const int ctas = C::CTAS_PER_SM * dev->num_sms;
+    if (workspace_bytes < size_t(ctas) * (2 * sea::pg::BKV + 3) * 4) return ATTN_ERR_INVALID;
+    p.ws_sum = static_cast<float*>(workspace);
+    p.ws_state = reinterpret_cast<int*>(p.ws_sum + size_t(ctas) * 2 * sea::pg::BKV);
+    if (launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::SMEM_BYTES, stream, tq, tk, p) != cudaSuccess ||
+        launch_pdl(sea::pg::paged_weights_merge_kernel, dim3(ctas), dim3(sea::pg::BKV), 0, stream, p) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+    return ATTN_OK;
   };
   using sea::pg::WeightCfg;
-  const cudaError_t err =
-      n == 16   ? launch(sea::pg::paged_weights_kernel<16>, WeightCfg<16>::THREADS, WeightCfg<16>::SMEM_BYTES)
-      : n == 32 ? launch(sea::pg::paged_weights_kernel<32>, WeightCfg<32>::THREADS, WeightCfg<32>::SMEM_BYTES)
-                : launch(sea::pg::paged_weights_kernel<128>, WeightCfg<128>::THREADS, WeightCfg<128>::SMEM_BYTES);
-  return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return n == 16   ? launch(sea::pg::paged_weights_kernel<16>, WeightCfg<16>{})
+         : n == 32 ? launch(sea::pg::paged_weights_kernel<32>, WeightCfg<32>{})
+                   : launch(sea::pg::paged_weights_kernel<128>, WeightCfg<128>{});
 }
 
 attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,

@@ -11,12 +11,15 @@
 // normaliser of a row is a column's constant that every thread reads from
 // shared memory.
 //   warps 0-3  one thread per slot: e^{s - lse} and the sums.
-//   warp 4     producer: K tiles of the CTA's K/V heads (one TMA copy per page,
-//              the table is read once), Q tiles and their normalisers.
+//   warp 4     producer: K tiles (one TMA copy per page, the table is read once
+//              per key tile), Q tiles and their normalisers.
 //   warp 5     tcgen05.mma issuer, into two S buffers in turn.
-// The (head, query tile) items of a key tile are dealt out to the CTAs of a
-// cluster of up to 8 where there are few key tiles; rank 0 adds the sums through
-// distributed shared memory.
+// An item is one S^T tile: (key tile, K/V head, query tile). The items of all
+// key tiles that some row sees lie in one line, in that order, cut into equal
+// shares, one per resident CTA, so prompts (whose first slots more rows see) and
+// ragged batches come out even. A key tile whose items fall into several shares
+// leaves partial sums in the workspace, which paged_weights_merge_kernel adds in
+// the order of the line.
 #pragma once
 
 #include "flash_attn.cuh"
@@ -31,6 +34,11 @@ struct WeightParams {
   const float* w_in;   // [batch, cap] or null (zeros)
   float* w_out;        // [batch, cap]
   float scale_log2;
+  fa::DivC dv_group;
+  int tiles;           // key tiles per sequence, by the table's size
+  float* ws_sum;       // [CTAs][2][128] sums of cut key tiles: one begun earlier, one that goes on
+  int* ws_state;       // [CTAs][3]: the tile begun earlier ends or passes here; the entry of the one
+                       // that goes on (-1: none), and in how many more shares
   uint32_t* err;
   uint64_t limit_ns;
 };
@@ -46,12 +54,12 @@ struct WeightCfg {
   static constexpr uint32_t TMEM_COLS = 2 * N;
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = OFF_K + K_STAGES * TILE_BYTES;
-  static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;  // [Q_STAGES][N] normalisers, log2 units
-  static constexpr int OFF_TOTAL = OFF_LSE + Q_STAGES * N * 4;  // [128] sums
-  static constexpr int OFF_BARS = OFF_TOTAL + BKV * 4;
+  static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;  // [Q_STAGES][N] -normaliser, log2 units
+  static constexpr int OFF_BARS = OFF_LSE + Q_STAGES * N * 4;
   // k_full[K], k_empty[K], q_full[Q], q_empty[Q], s_full[2], s_free[2], drain
   static constexpr int NUM_BARS = 2 * K_STAGES + 2 * Q_STAGES + 5;
-  static constexpr int OFF_MISC = OFF_BARS + 8 * NUM_BARS;
+  static constexpr int OFF_SCAN = OFF_BARS + 8 * NUM_BARS;  // long long [8], then what locate() found
+  static constexpr int OFF_MISC = OFF_SCAN + 8 * 8 + 32;
   static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 16;
 };
 
@@ -92,6 +100,120 @@ __device__ __forceinline__ Tokens tokens_seeing(const Geo& g, const Seq& s, int 
   return t;
 }
 
+// A key tile's place in the line: entry b * tiles + tile, and its items.
+struct Entry {
+  int b, tile;
+  Seq s;
+  Tokens seen;
+  int chunks, items;   // query tiles that see it, times K/V heads
+};
+
+__device__ __forceinline__ void entry_at(const WeightParams& p, Entry& e, int b, int tile) {
+  const Geo& g = p.g;
+  if (b != e.b) {
+    e.b = b;
+    e.s = seq_of(g, b);
+  }
+  e.tile = tile;
+  e.seen = tokens_seeing(g, e.s, tile * BKV, (tile + 1) * BKV);
+  e.chunks = (e.seen.hi - e.seen.lo + g.tok_per_tile - 1) / g.tok_per_tile;
+  e.items = e.chunks * g.kv_heads;
+}
+
+// The next entry with items. Sequences end at their last slot, and no row sees
+// what lies between the first slots and the window of row 0.
+__device__ __forceinline__ bool entry_next(const WeightParams& p, Entry& e) {
+  const Geo& g = p.g;
+  int b = e.b, tile = e.tile;
+  do {
+    ++tile;
+    if (g.window && tile * BKV >= g.first) tile = max(tile, max(0, e.s.off - g.window + 1) / BKV);
+    if (tile >= p.tiles || tile * BKV >= e.s.kv) {
+      if (++b >= g.batch) return false;
+      tile = 0;
+    }
+    entry_at(p, e, b, tile);
+  } while (e.items == 0);
+  return true;
+}
+
+// A CTA's share of the line, entry by entry: items [i0, i1) of entry e.
+struct Share {
+  Entry e;
+  long long left;      // items of the share from i0 on
+  int i0, i1;
+  __device__ __forceinline__ void cut() {
+    i1 = static_cast<int>(min(static_cast<long long>(e.items), i0 + left));
+  }
+  __device__ __forceinline__ bool next(const WeightParams& p) {
+    left -= i1 - i0;
+    if (left <= 0 || !entry_next(p, e)) return false;
+    i0 = 0;
+    cut();
+    return true;
+  }
+};
+
+// The whole CTA: where share `cta` of `ctas` begins. Each thread adds up the items of a
+// run of entries; the thread whose run holds the share's first item finds it.
+struct Located {
+  long long per, left;
+  int b, tile, i0;
+};
+
+__device__ __forceinline__ void locate(const WeightParams& p, int cta, int ctas, int threads, long long* scan,
+                                       Located* found) {
+  const Geo& g = p.g;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int entries = g.batch * p.tiles;
+  const int run = (entries + threads - 1) / threads;
+  const int a = min(entries, t * run), z = min(entries, a + run);
+  Entry e;
+  e.b = -1;
+  long long mine = 0;
+  auto skip = [&](int x) {  // entries behind the end of a sequence hold nothing
+    const int b = x / p.tiles, tile = x - b * p.tiles;
+    entry_at(p, e, b, tile);
+    return tile * BKV >= e.s.kv ? (b + 1) * p.tiles : x + 1;
+  };
+  for (int x = a; x < z;) {
+    const int nx = skip(x);
+    mine += e.items;
+    x = nx;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+  for (int i = 0; i < threads / 32; ++i) {
+    if (i < warp) before += scan[i];
+    total += scan[i];
+  }
+  const long long per = (total + ctas - 1) / ctas;
+  const long long pos = per * cta;
+  if (t == 0) {
+    found->per = per;
+    found->left = max(0ll, min(per, total - pos));
+  }
+  if (pos < total && pos >= before && pos < before + mine) {
+    for (int x = a; x < z;) {
+      const int nx = skip(x);
+      if (before + e.items > pos) break;
+      before += e.items;
+      x = nx;
+    }
+    found->b = e.b;
+    found->tile = e.tile;
+    found->i0 = static_cast<int>(pos - before);
+  }
+  __syncthreads();
+}
+
 template <int N>
 __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_SM)
     paged_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -110,14 +232,10 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
   auto s_free = [&](int s) { return bar0 + 8u * (2 * KS + 2 * QS + 2 + s); };
   const uint32_t drain_bar = bar0 + 8u * (2 * KS + 2 * QS + 4);
   float* lse_ring = reinterpret_cast<float*>(smem + C::OFF_LSE);
-  float* total = reinterpret_cast<float*>(smem + C::OFF_TOTAL);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
   const Geo& g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // Key tiles are the slowest grid dimension: those that most rows see start first.
-  const int rank = blockIdx.x, ranks = gridDim.x, b = blockIdx.y, tile = blockIdx.z;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
       mbar_init(k_full(s), 1);
@@ -149,45 +267,61 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
   griddep_launch_dependents();
   const WaitCtl wc{abort_flag, p.err, p.limit_ns};
 
-  const Seq s = seq_of(g, b);
-  const Tokens seen = tokens_seeing(g, s, tile * BKV, (tile + 1) * BKV);
-  const int chunks = (seen.hi - seen.lo + g.tok_per_tile - 1) / g.tok_per_tile;
-  // This rank's items, head by head: item = head * chunks + query tile.
-  const int items = g.kv_heads * chunks;
-  const int i0 = static_cast<int>(static_cast<long long>(items) * rank / ranks);
-  const int i1 = static_cast<int>(static_cast<long long>(items) * (rank + 1) / ranks);
+  Located* found = reinterpret_cast<Located*>(smem + C::OFF_SCAN + 64);
+  locate(p, blockIdx.x, gridDim.x, C::THREADS, reinterpret_cast<long long*>(smem + C::OFF_SCAN), found);
+  Share w;
+  w.e.b = -1;
+  w.left = found->left;
+  const long long per = found->per;
+  if (w.left > 0) {
+    entry_at(p, w.e, found->b, found->tile);
+    w.i0 = found->i0;
+    w.cut();
+  }
 
-  if (warp == 4) {
+  if (warp == 4 && w.left > 0) {
     // ---------------- producer ----------------
     const int n_pages = pages_per_tile(g);
     const uint32_t page_bytes = TILE_BYTES / n_pages;
-    PageLoad l{false, 0};
-    if (i0 < i1 && lane < n_pages) {
-      Span all{};
-      all.hi = s.kv;
-      l = page_of_tile(g, b, all, tile, lane);
-    }
-    const uint32_t k_bytes = __popc(__ballot_sync(0xffffffffu, l.load)) * page_bytes;
     const uint32_t q_bytes = static_cast<uint32_t>(g.tok_per_tile * g.group) * DH * 2;
+    // Normalisers of an item's rows, negated, read an item ahead: each costs a
+    // round trip to L2. -inf takes a row's weight to zero.
+    constexpr int LANE_ROWS = (N + 31) / 32;
+    const int q_rows = g.tok_per_tile * g.group;
+    int row_tok[LANE_ROWS], row_head[LANE_ROWS];  // this lane's rows of a query tile
+#pragma unroll
+    for (int x = 0; x < LANE_ROWS; ++x) {
+      const int r = 32 * x + lane;
+      row_tok[x] = r < q_rows ? fa::div_c(r, p.dv_group) : g.t_q;
+      row_head[x] = r - row_tok[x] * g.group;
+    }
+    float norm[LANE_ROWS];
+    auto read_norms = [&](int i) {
+      const int h = i / w.e.chunks;
+      const int tok0 = w.e.seen.lo + (i - h * w.e.chunks) * g.tok_per_tile;
+#pragma unroll
+      for (int x = 0; x < LANE_ROWS; ++x) {
+        const int tok = tok0 + row_tok[x];
+        norm[x] = -INFINITY;
+        if (i < w.i1 && tok < w.e.seen.hi)
+          norm[x] = __ldg(p.lse + (static_cast<int64_t>(w.e.b) * g.t_q + tok) * g.n_heads + h * g.group + row_head[x]);
+      }
+    };
     int kn = 0, qn = 0;
     bool ok = true;
-    for (int i = i0; i < i1; ++i) {
-      const int h = i / chunks, ch = i - h * chunks;
-      const int tok0 = seen.lo + ch * g.tok_per_tile;
-      // normalisers of the tile's rows; +inf takes a row's weight to zero
-      float lse2[(N + 31) / 32];
-#pragma unroll
-      for (int x = 0; x < (N + 31) / 32; ++x) {
-        const int r = 32 * x + lane;
-        const int tok = tok0 + r / g.group;
-        lse2[x] = INFINITY;
-        if (r < N && tok < seen.hi && r < g.tok_per_tile * g.group) {
-          const float v =
-              __ldg(p.lse + (static_cast<int64_t>(b) * g.t_q + tok) * g.n_heads + h * g.group + r % g.group);
-          if (v != -INFINITY) lse2[x] = v * kLog2e;
-        }
-      }
-      if (i == i0 || ch == 0) {  // the next head's K
+    do {
+    PageLoad l{false, 0};
+    if (lane < n_pages) {
+      Span all{};
+      all.hi = w.e.s.kv;
+      l = page_of_tile(g, w.e.b, all, w.e.tile, lane);
+    }
+    read_norms(w.i0);
+    const uint32_t k_bytes = __popc(__ballot_sync(0xffffffffu, l.load)) * page_bytes;
+    for (int i = w.i0; i < w.i1; ++i) {
+      const int h = i / w.e.chunks, ch = i - h * w.e.chunks;
+      const int tok0 = w.e.seen.lo + ch * g.tok_per_tile;
+      if (i == w.i0 || ch == 0) {  // the next head's K
         const int st = kn % KS;
         ok = __all_sync(0xffffffffu, mbar_wait(k_empty(st), ((kn / KS) & 1) ^ 1u, wc));
         if (!ok) break;
@@ -200,56 +334,73 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       ok = __all_sync(0xffffffffu, mbar_wait(q_empty(st), ((qn / QS) & 1) ^ 1u, wc));
       if (!ok) break;
 #pragma unroll
-      for (int x = 0; x < (N + 31) / 32; ++x)
-        if (32 * x + lane < N) lse_ring[st * N + 32 * x + lane] = lse2[x];
+      for (int x = 0; x < LANE_ROWS; ++x)
+        if (32 * x + lane < N)
+          lse_ring[st * N + 32 * x + lane] = norm[x] == -INFINITY ? -INFINITY : -norm[x] * kLog2e;
+      read_norms(i + 1);
       __syncwarp();
       if (lane == 0) {
         mbar_arrive_expect_tx(q_full(st), q_bytes);
-        tma_load_4d(sbase + C::OFF_Q + st * C::Q_BYTES, &tm_q, q_full(st), 0, h * g.group, tok0, b);
+        tma_load_4d(sbase + C::OFF_Q + st * C::Q_BYTES, &tm_q, q_full(st), 0, h * g.group, tok0, w.e.b);
       }
       ++qn;
     }
+    } while (ok && w.next(p));
     // Let the last copies land before the CTA may exit.
     for (int i = max(0, kn - KS); i < kn; ++i) mbar_wait_drain(k_full(i % KS), (i / KS) & 1, p.limit_ns);
     for (int i = max(0, qn - QS); i < qn; ++i) mbar_wait_drain(q_full(i % QS), (i / QS) & 1, p.limit_ns);
-  } else if (warp == 5) {
+  } else if (warp == 5 && w.left > 0) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16_f32(BKV, N, 0, 0);  // K and Q both K-major
       int kn = 0, n = 0;
-      for (int i = i0; i < i1; ++i, ++n) {
-        const bool head_starts = i == i0 || i % chunks == 0;
-        const bool head_ends = i + 1 == i1 || (i + 1) % chunks == 0;
-        if (head_starts) {
-          if (!mbar_wait(k_full(kn % KS), (kn / KS) & 1, wc)) break;
-          ++kn;
-        }
-        const int ks = (kn - 1) % KS, qs = n % QS, buf = n & 1;
-        if (!mbar_wait(q_full(qs), (n / QS) & 1, wc)) break;
-        if (!mbar_wait(s_free(buf), ((n >> 1) & 1) ^ 1u, wc)) break;
-        tc_fence_after();
+      bool ok = true;
+      do {
+        int ch = w.i0 % w.e.chunks;
+        for (int i = w.i0; i < w.i1 && ok; ++i, ++n) {
+          if (i == w.i0 || ch == 0) {
+            ok = mbar_wait(k_full(kn % KS), (kn / KS) & 1, wc);
+            ++kn;
+          }
+          const int ks = (kn - 1) % KS, qs = n % QS, buf = n & 1;
+          ok = ok && mbar_wait(q_full(qs), (n / QS) & 1, wc) && mbar_wait(s_free(buf), ((n >> 1) & 1) ^ 1u, wc);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          mma_f16_ss(tmem_base + buf * N, smem_desc_sw128(sbase + C::OFF_K + ks * TILE_BYTES + kk * 32, 16, 1024),
-                     smem_desc_sw128(sbase + C::OFF_Q + qs * C::Q_BYTES + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
-        mma_commit(s_full(buf));
-        mma_commit(q_empty(qs));
-        if (head_ends) mma_commit(k_empty(ks));
-      }
+          for (int kk = 0; kk < DH / 16; ++kk)
+            mma_f16_ss(tmem_base + buf * N, smem_desc_sw128(sbase + C::OFF_K + ks * TILE_BYTES + kk * 32, 16, 1024),
+                       smem_desc_sw128(sbase + C::OFF_Q + qs * C::Q_BYTES + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+          mma_commit(s_full(buf));
+          mma_commit(q_empty(qs));
+          if (++ch == w.e.chunks) ch = 0;
+          if (ch == 0 || i + 1 == w.i1) mma_commit(k_empty(ks));
+        }
+      } while (ok && w.next(p));
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0, p.limit_ns);
     }
-  } else {
+  } else if (warp < 4) {
     // ---------------- weights: thread = slot ----------------
-    const int j = tile * BKV + threadIdx.x;
-    const Tokens mine = tokens_seeing(g, s, j, j + 1);
-    float sum = 0.f;
     const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    const int t = threadIdx.x;
     int n = 0;
-    for (int i = i0; i < i1; ++i, ++n) {
+    int begun = 0, on = -1, more = 0;  // for the merge: see ws_state
+    bool ok = true;
+    if (w.left > 0) do {
+    const int j = w.e.tile * BKV + t;
+    const Tokens mine = tokens_seeing(g, w.e.s, j, j + 1);
+    // A slot in a hole, or behind the end, has none (its K may be anything).
+    int page = -1;
+    if (j < w.e.s.kv) page = __ldg(g.table + static_cast<int64_t>(w.e.b) * g.pages_per_seq + (j >> g.page_shift));
+    const int64_t at = static_cast<int64_t>(w.e.b) * g.cap + j;
+    const bool whole = w.i0 == 0 && w.i1 == w.e.items;
+    const float w_old = whole && j < g.cap && p.w_in != nullptr ? p.w_in[at] : 0.f;
+    float sum = 0.f;
+    int ch = w.i0 % w.e.chunks;
+    for (int i = w.i0; i < w.i1; ++i, ++n) {
       const int qs = n % QS, buf = n & 1;
-      if (!mbar_wait(q_full(qs), (n / QS) & 1, wc)) break;  // the producer's normalisers
-      if (!mbar_wait(s_full(buf), (n >> 1) & 1, wc)) break;
+      ok = mbar_wait(q_full(qs), (n / QS) & 1, wc) && mbar_wait(s_full(buf), (n >> 1) & 1, wc);  // normalisers, scores
+      if (!ok) break;
       tc_fence_after();
       float x[N];
       {
@@ -262,7 +413,8 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       __syncwarp();
       if (lane == 0) mbar_arrive(s_free(buf));
       // Columns [c_lo, c_hi) are rows that see this slot.
-      const int tok0 = seen.lo + (i % chunks) * g.tok_per_tile;
+      const int tok0 = w.e.seen.lo + ch * g.tok_per_tile;
+      if (++ch == w.e.chunks) ch = 0;
       const int c_lo = (mine.lo - tok0) * g.group;
       const int c_hi = min(mine.hi - tok0, g.tok_per_tile) * g.group;
       if (c_lo > 0) {
@@ -282,8 +434,8 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       for (int e = 0; e < N; e += 4) {
         const float4 v = norm[e / 4];
         float y0, y1, y2, y3;
-        f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), sl2x2, f2_pack(-v.x, -v.y)), y0, y1);
-        f2_unpack(f2_fma(f2_pack(x[e + 2], x[e + 3]), sl2x2, f2_pack(-v.z, -v.w)), y2, y3);
+        f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), sl2x2, f2_pack(v.x, v.y)), y0, y1);
+        f2_unpack(f2_fma(f2_pack(x[e + 2], x[e + 3]), sl2x2, f2_pack(v.z, v.w)), y2, y3);
         acc2[0] = f2_add(acc2[0], f2_pack(ex2_approx(y0), ex2_approx(y1)));
         acc2[1] = f2_add(acc2[1], f2_pack(ex2_approx(y2), ex2_approx(y3)));
       }
@@ -293,35 +445,63 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty(qs));
     }
-    // A slot in a hole, or behind the end, has none (its K may be anything).
-    bool held = j < s.kv;
-    if (held) {
-      const int page = __ldg(g.table + static_cast<int64_t>(b) * g.pages_per_seq + (j >> g.page_shift));
-      held = page >= 0 && page < g.num_pages;
+    if (page < 0 || page >= g.num_pages) sum = 0.f;
+    if (whole) {
+      if (j < g.cap) p.w_out[at] = w_old + sum;
+    } else {
+      const bool starts = w.i0 == 0;
+      p.ws_sum[(2 * static_cast<int64_t>(blockIdx.x) + (starts ? 1 : 0)) * BKV + t] = sum;
+      if (starts) {
+        on = w.e.b * p.tiles + w.e.tile;
+        more = static_cast<int>((w.e.items - w.i1 + per - 1) / per);
+      } else {
+        begun = 1;
+      }
     }
-    total[threadIdx.x] = held ? sum : 0.f;
+    } while (ok && w.next(p));
+    if (t == 0) {
+      p.ws_state[3 * blockIdx.x] = begun;
+      p.ws_state[3 * blockIdx.x + 1] = on;
+      p.ws_state[3 * blockIdx.x + 2] = more;
+    }
+    // Slots of key tiles that no row sees keep their weights.
+    if (p.w_in != p.w_out) {
+      Entry e;
+      e.b = -1;
+      for (int x = blockIdx.x; x < g.batch * p.tiles; x += gridDim.x) {
+        entry_at(p, e, x / p.tiles, x % p.tiles);
+        const int j = e.tile * BKV + t;
+        if (e.items > 0 || j >= g.cap) continue;
+        const int64_t at = static_cast<int64_t>(e.b) * g.cap + j;
+        p.w_out[at] = p.w_in != nullptr ? p.w_in[at] : 0.f;
+      }
+    }
   }
 
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (ranks > 1) cluster_sync();
-  const int t = threadIdx.x;
-  if (rank == 0 && t < BKV && tile * BKV + t < g.cap) {
-    float v = total[t];
-    for (int i = 1; i < ranks; ++i) {
-      float x;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(smem_u32(&total[t]), i)) : "memory");
-      v += x;
-    }
-    const int64_t at = static_cast<int64_t>(b) * g.cap + tile * BKV + t;
-    p.w_out[at] = (p.w_in != nullptr ? p.w_in[at] : 0.f) + v;
-  }
-  if (ranks > 1) cluster_sync();  // no CTA leaves while rank 0 still reads its sums
   if (warp == 5) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+}
+
+// Adds up the key tiles that were cut: block c the one that begins in share c.
+__global__ void __launch_bounds__(BKV) paged_weights_merge_kernel(const WeightParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int c = blockIdx.x, t = threadIdx.x;
+  const int entry = p.ws_state[3 * c + 1];
+  if (entry < 0) return;
+  const int more = p.ws_state[3 * c + 2];
+  const int b = entry / p.tiles, j = (entry - b * p.tiles) * BKV + t;
+  float v = p.ws_sum[(2 * static_cast<int64_t>(c) + 1) * BKV + t];
+#pragma unroll 4
+  for (int i = 1; i <= more; ++i) v += p.ws_sum[2 * static_cast<int64_t>(c + i) * BKV + t];
+  if (j >= p.g.cap) return;
+  const int64_t at = static_cast<int64_t>(b) * p.g.cap + j;
+  p.w_out[at] = (p.w_in != nullptr ? p.w_in[at] : 0.f) + v;
 }
 
 }  // namespace pg

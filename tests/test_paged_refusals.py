@@ -47,7 +47,7 @@ def test_every_entry_rejects_a_bad_cache(lib, kw):
     bad = cache(**kw)
     assert call_paged(lib, c=bad) == attn.ATTN_ERR_INVALID
     assert lib.attn_paged_append(m(Q, 128), m(OUT, 128), bad, 1, 4, 0, None) == attn.ATTN_ERR_INVALID
-    assert lib.attn_paged_weights(m(Q, 256), bad, 1, 4, 4, mask(), LSE, 0.125, W1, W2, None) == attn.ATTN_ERR_INVALID
+    assert lib.attn_paged_weights(m(Q, 256), bad, 1, 4, 4, mask(), LSE, 0.125, W1, W2, WS, 1 << 30, None) == attn.ATTN_ERR_INVALID
     good = cache(k=m(KP2, 128), v=m(VP2, 128), table=TBL2, lens=LENS2)
     assert lib.attn_paged_evict(bad, 1, 16, 0, 0, W1, good, W2, KEPT, None) == attn.ATTN_ERR_INVALID
     assert lib.attn_paged_evict(good, 1, 16, 0, 0, W1, bad, W2, KEPT, None) == attn.ATTN_ERR_INVALID
@@ -78,12 +78,12 @@ def test_append_rejects_invalid_arguments(lib, kw):
 @pytest.mark.parametrize("kw", [
     dict(batch=0), dict(t_q=0), dict(heads=3), dict(q=m(Q, 100)), dict(lse=0), dict(lse=LSE + 2), dict(w_out=0),
     dict(w_out=W2 + 1), dict(w_in=W1 + 2), dict(w_in=W2 + 4), dict(w_out=Q), dict(w_out=LSE), dict(w_out=KP),
-    dict(scale=-1.0), dict(mk=mask(first=1)),
+    dict(scale=-1.0), dict(mk=mask(first=1)), dict(ws=0), dict(ws=WS + 4),
 ])
 def test_weights_rejects_invalid_arguments(lib, kw):
     st = lib.attn_paged_weights(kw.get("q", m(Q, 256)), cache(), kw.get("batch", 1), kw.get("t_q", 4),
                                 kw.get("heads", 4), kw.get("mk", mask()), kw.get("lse", LSE), kw.get("scale", 0.125),
-                                kw.get("w_in", W1), kw.get("w_out", W2), None)
+                                kw.get("w_in", W1), kw.get("w_out", W2), kw.get("ws", WS), 1 << 30, None)
     assert st == attn.ATTN_ERR_INVALID
 
 
