@@ -10,10 +10,12 @@
 // weights are summed by one thread, in a fixed order, with no shuffles; the
 // normaliser of a row is a column's constant that every thread reads from
 // shared memory.
-//   warps 0-3  one thread per slot: e^{s - lse} and the sums.
-//   warp 4     producer: K tiles (one TMA copy per page, the table is read once
+//   warps 0-3  one thread per slot: e^{s - lse} and the sums. N = 128 has two such
+//              groups, 64 columns each: four warps per scheduler keep the
+//              exponential unit busier than two.
+//   then       a producer warp: K tiles (one TMA copy per page, the table is read once
 //              per key tile), Q tiles and their normalisers.
-//   warp 5     tcgen05.mma issuer, into two S buffers in turn.
+//   last       a tcgen05.mma issuer, into two S buffers in turn.
 // An item is one S^T tile: (key tile, K/V head, query tile). The items of all
 // key tiles that some row sees lie in one line, in that order, cut into equal
 // shares, one per resident CTA, so prompts (whose first slots more rows see) and
@@ -46,7 +48,10 @@ struct WeightParams {
 template <int N_>
 struct WeightCfg {
   static constexpr int N = N_;
-  static constexpr int THREADS = 192;
+  static constexpr int SPLIT = N == 128 ? 2 : 1;  // column halves, each with its own four warps
+  static constexpr int NC = N / SPLIT;            // columns of a thread
+  static constexpr int WARPS = 4 * SPLIT;
+  static constexpr int THREADS = 32 * (WARPS + 2);
   static constexpr int K_STAGES = N == 128 ? 2 : 3;
   static constexpr int Q_STAGES = 3;
   static constexpr int CTAS_PER_SM = N == 128 ? 2 : 4;
@@ -56,17 +61,18 @@ struct WeightCfg {
   static constexpr int OFF_Q = OFF_K + K_STAGES * TILE_BYTES;
   static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;  // [Q_STAGES][N] -normaliser, log2 units
   static constexpr int OFF_BARS = OFF_LSE + Q_STAGES * N * 4;
-  // k_full[K], k_empty[K], q_full[Q], q_empty[Q], s_full[2], s_free[2], drain
-  static constexpr int NUM_BARS = 2 * K_STAGES + 2 * Q_STAGES + 5;
-  static constexpr int OFF_SCAN = OFF_BARS + 8 * NUM_BARS;  // long long [8], then what locate() found
-  static constexpr int OFF_MISC = OFF_SCAN + 8 * 8 + 32;
+  // k_full[K], k_empty[K], q_full[Q], q_empty[Q], s_full[2], s_free[2], drain, half_full, half_empty
+  static constexpr int NUM_BARS = 2 * K_STAGES + 2 * Q_STAGES + 7;
+  static constexpr int OFF_SCAN = OFF_BARS + 8 * NUM_BARS;  // long long [10], then what locate() found
+  static constexpr int OFF_HALF = OFF_SCAN + 8 * 10 + 32;   // [128] the second half's sums
+  static constexpr int OFF_MISC = OFF_HALF + (SPLIT == 2 ? BKV * 4 : 0);
   static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 16;
 };
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 128) {
-    tmem_ld128(taddr, r);
+  if constexpr (N == 64) {
+    tmem_ld64(taddr, r);
   } else if constexpr (N == 32) {
     tmem_ld32(taddr, r);
   } else {
@@ -231,6 +237,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
   auto s_full = [&](int s) { return bar0 + 8u * (2 * KS + 2 * QS + s); };
   auto s_free = [&](int s) { return bar0 + 8u * (2 * KS + 2 * QS + 2 + s); };
   const uint32_t drain_bar = bar0 + 8u * (2 * KS + 2 * QS + 4);
+  const uint32_t half_full = drain_bar + 8u, half_empty = drain_bar + 16u;
   float* lse_ring = reinterpret_cast<float*>(smem + C::OFF_LSE);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 4);
@@ -243,19 +250,21 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     }
     for (int s = 0; s < QS; ++s) {
       mbar_init(q_full(s), 1);
-      mbar_init(q_empty(s), 5);  // the MMA and the four warps that read the normalisers
+      mbar_init(q_empty(s), 1 + C::WARPS);  // the MMA and the warps that read the normalisers
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
-      mbar_init(s_free(s), 4);
+      mbar_init(s_free(s), C::WARPS);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(half_full, 4);
+    mbar_init(half_empty, 4);
     *abort_flag = 0u;
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
   }
-  if (warp == 5) {
+  if (warp == C::WARPS + 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
   griddep_launch_dependents();
   const WaitCtl wc{abort_flag, p.err, p.limit_ns};
 
-  Located* found = reinterpret_cast<Located*>(smem + C::OFF_SCAN + 64);
+  Located* found = reinterpret_cast<Located*>(smem + C::OFF_SCAN + 80);
   locate(p, blockIdx.x, gridDim.x, C::THREADS, reinterpret_cast<long long*>(smem + C::OFF_SCAN), found);
   Share w;
   w.e.b = -1;
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     w.cut();
   }
 
-  if (warp == 4 && w.left > 0) {
+  if (warp == C::WARPS && w.left > 0) {
     // ---------------- producer ----------------
     const int n_pages = pages_per_tile(g);
     const uint32_t page_bytes = TILE_BYTES / n_pages;
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     // Let the last copies land before the CTA may exit.
     for (int i = max(0, kn - KS); i < kn; ++i) mbar_wait_drain(k_full(i % KS), (i / KS) & 1, p.limit_ns);
     for (int i = max(0, qn - QS); i < qn; ++i) mbar_wait_drain(q_full(i % QS), (i / QS) & 1, p.limit_ns);
-  } else if (warp == 5 && w.left > 0) {
+  } else if (warp == C::WARPS + 1 && w.left > 0) {
     if (lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_f16_f32(BKV, N, 0, 0);  // K and Q both K-major
@@ -379,11 +388,14 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       mma_commit(drain_bar);
       mbar_wait_drain(drain_bar, 0, p.limit_ns);
     }
-  } else if (warp < 4) {
+  } else if (warp < C::WARPS) {
     // ---------------- weights: thread = slot ----------------
-    const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
-    const int t = threadIdx.x;
-    int n = 0;
+    constexpr int NC = C::NC;
+    const int half = warp >> 2;  // columns [half * NC, half * NC + NC)
+    const uint32_t s_tmem = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * NC;
+    const int t = threadIdx.x & (BKV - 1);
+    float* half_sum = reinterpret_cast<float*>(smem + C::OFF_HALF);
+    int n = 0, entry_n = 0;
     int begun = 0, on = -1, more = 0;  // for the merge: see ws_state
     bool ok = true;
     if (w.left > 0) do {
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     if (j < w.e.s.kv) page = __ldg(g.table + static_cast<int64_t>(w.e.b) * g.pages_per_seq + (j >> g.page_shift));
     const int64_t at = static_cast<int64_t>(w.e.b) * g.cap + j;
     const bool whole = w.i0 == 0 && w.i1 == w.e.items;
-    const float w_old = whole && j < g.cap && p.w_in != nullptr ? p.w_in[at] : 0.f;
+    const float w_old = whole && half == 0 && j < g.cap && p.w_in != nullptr ? p.w_in[at] : 0.f;
     float sum = 0.f;
     int ch = w.i0 % w.e.chunks;
     for (int i = w.i0; i < w.i1; ++i, ++n) {
@@ -402,12 +414,12 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       ok = mbar_wait(q_full(qs), (n / QS) & 1, wc) && mbar_wait(s_full(buf), (n >> 1) & 1, wc);  // normalisers, scores
       if (!ok) break;
       tc_fence_after();
-      float x[N];
+      float x[NC];
       {
-        uint32_t r[N];
-        tmem_ld_cols<N>(s_tmem + buf * N, r);
+        uint32_t r[NC];
+        tmem_ld_cols<NC>(s_tmem + buf * N, r);
 #pragma unroll
-        for (int e = 0; e < N; ++e) x[e] = __uint_as_float(r[e]);
+        for (int e = 0; e < NC; ++e) x[e] = __uint_as_float(r[e]);
       }
       tc_fence_before();
       __syncwarp();
@@ -415,23 +427,23 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       // Columns [c_lo, c_hi) are rows that see this slot.
       const int tok0 = w.e.seen.lo + ch * g.tok_per_tile;
       if (++ch == w.e.chunks) ch = 0;
-      const int c_lo = (mine.lo - tok0) * g.group;
-      const int c_hi = min(mine.hi - tok0, g.tok_per_tile) * g.group;
+      const int c_lo = (mine.lo - tok0) * g.group - half * NC;
+      const int c_hi = min(mine.hi - tok0, g.tok_per_tile) * g.group - half * NC;
       if (c_lo > 0) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
+        for (int e = 0; e < NC; ++e)
           if (e < c_lo) x[e] = -INFINITY;
       }
-      if (c_hi < N) {
+      if (c_hi < NC) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
+        for (int e = 0; e < NC; ++e)
           if (e >= c_hi) x[e] = -INFINITY;
       }
-      const float4* norm = reinterpret_cast<const float4*>(lse_ring + qs * N);
+      const float4* norm = reinterpret_cast<const float4*>(lse_ring + qs * N + half * NC);
       const uint64_t sl2x2 = f2_pack(p.scale_log2, p.scale_log2);
       uint64_t acc2[2] = {0ull, 0ull};
 #pragma unroll
-      for (int e = 0; e < N; e += 4) {
+      for (int e = 0; e < NC; e += 4) {
         const float4 v = norm[e / 4];
         float y0, y1, y2, y3;
         f2_unpack(f2_fma(f2_pack(x[e], x[e + 1]), sl2x2, f2_pack(v.x, v.y)), y0, y1);
@@ -446,6 +458,22 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       if (lane == 0) mbar_arrive(q_empty(qs));
     }
     if (page < 0 || page >= g.num_pages) sum = 0.f;
+    if constexpr (C::SPLIT == 2) {
+      if (!ok) break;
+      if (half == 1) {
+        ok = mbar_wait(half_empty, (entry_n & 1) ^ 1u, wc);
+        half_sum[t] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(half_full);
+      } else {
+        ok = mbar_wait(half_full, entry_n & 1, wc);
+        sum += half_sum[t];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(half_empty);
+      }
+      ++entry_n;
+      if (half == 1) continue;
+    }
     if (whole) {
       if (j < g.cap) p.w_out[at] = w_old + sum;
     } else {
@@ -459,13 +487,13 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       }
     }
     } while (ok && w.next(p));
-    if (t == 0) {
+    if (threadIdx.x == 0) {
       p.ws_state[3 * blockIdx.x] = begun;
       p.ws_state[3 * blockIdx.x + 1] = on;
       p.ws_state[3 * blockIdx.x + 2] = more;
     }
     // Slots of key tiles that no row sees keep their weights.
-    if (p.w_in != p.w_out) {
+    if (p.w_in != p.w_out && half == 0) {
       Entry e;
       e.b = -1;
       for (int x = blockIdx.x; x < g.batch * p.tiles; x += gridDim.x) {
@@ -481,7 +509,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == C::WARPS + 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
