@@ -20,6 +20,7 @@ and, on a paged K/V cache (PagedKV),
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -154,6 +155,8 @@ class AttnError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Loads libattn.so (built in-tree by ``python -m speech_encoder_attention_b200.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -412,44 +415,40 @@ def _q_lens_ptr(q_lens, batch, device) -> int:
     return 0 if q_lens is None else _dev_tensor(q_lens, "q_lens", torch.int32, (batch,), device)
 
 
-class _On:
+@contextlib.contextmanager
+def _on(device, stream):
     """The tensors' device and the call's stream as the current ones, so that
-    what is allocated and launched belongs to them. Entering yields the stream."""
-    __slots__ = ("ctx", "index")
+    what is allocated and launched belongs to them."""
+    import torch
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+            return
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {device}")
+        with torch.cuda.stream(stream):
+            yield
 
-    def __init__(self, device, stream):
-        import torch
-        self.index = device.index
-        self.ctx = ()
-        if torch.cuda.current_device() != device.index:
-            self.ctx = (torch.cuda.device(device),)
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the cache on {device}")
-            self.ctx += (torch.cuda.stream(stream),)
 
-    def __enter__(self):
-        import torch
-        for c in self.ctx:
-            c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+def _elsewhere(torch, device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or torch._C._cuda_getDevice() != device.index
 
 
 def attn_paged_append(k_new, v_new, cache: PagedKV, batch, t_new, q_lens=None, stream=None) -> None:
     """Writes a chunk's K and V rows ([batch*t_new, n_kv_heads*64] fp16, or column
     views) into the slots at the end of each sequence; cache.lens already counts
     them, q_lens ([batch] int32) says how many of the t_new rows are valid."""
-    lib = load_library()
-    kv = _batch_of(cache, batch)
+    import torch
     dev, cols = cache.device, cache.n_kv_heads * HEAD_DIM
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return attn_paged_append(k_new, v_new, cache, batch, t_new, q_lens)
+    kv = _batch_of(cache, batch)
     kn, vn = _rows(k_new, "k_new", batch * t_new, cols, dev), _rows(v_new, "v_new", batch * t_new, cols, dev)
     lens = _q_lens_ptr(q_lens, batch, dev)
-    with _On(dev, stream) as s:
-        _check(lib.attn_paged_append(kn, vn, kv, batch, t_new, lens, s), "attn_paged_append")
+    st = load_library().attn_paged_append(kn, vn, kv, batch, t_new, lens, torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(st, "attn_paged_append")
 
 
 def paged_workspace_size(batch, t_q, n_heads, n_kv_heads) -> int:
@@ -475,29 +474,32 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
     [batch*t_q, n_heads] fp32, the log of each row's softmax denominator.
     Without workspace one is allocated for the call."""
     import torch
+    dev, rows, cols = cache.device, batch * t_q, n_heads * HEAD_DIM
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return attn_paged(q, cache, batch, t_q, n_heads, window, first, causal, q_lens, sinks, scale, out,
+                              return_lse, lse, workspace)
     lib = load_library()
     kv = _batch_of(cache, batch)
-    dev, rows, cols = cache.device, batch * t_q, n_heads * HEAD_DIM
     qm = _rows(q, "q", rows, cols, dev)
     mask = AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, dev))
     sinks_ptr = 0 if sinks is None else _dev_tensor(sinks, "sinks", torch.float32, (n_heads,), dev)
-    with _On(dev, stream) as s:
-        if out is None:
-            out = q.new_empty((rows, cols))
-            om = AttnMat(out.data_ptr(), cols)
-        else:
-            om = _rows(out, "out", rows, cols, dev)
-        if lse is not None:
-            lse_ptr = _dev_tensor(lse, "lse", torch.float32, (rows, n_heads), dev)
-        elif return_lse:
-            lse = q.new_empty((rows, n_heads), dtype=torch.float32)
-            lse_ptr = lse.data_ptr()
-        else:
-            lse_ptr = 0
-        workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
-        st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, scale, om, lse_ptr,
-                            workspace.data_ptr(), ws_bytes, s)
-        _check(st, "attn_paged")
+    if out is None:
+        out = q.new_empty((rows, cols))
+        om = AttnMat(out.data_ptr(), cols)
+    else:
+        om = _rows(out, "out", rows, cols, dev)
+    if lse is not None:
+        lse_ptr = _dev_tensor(lse, "lse", torch.float32, (rows, n_heads), dev)
+    elif return_lse:
+        lse = q.new_empty((rows, n_heads), dtype=torch.float32)
+        lse_ptr = lse.data_ptr()
+    else:
+        lse_ptr = 0
+    workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
+    st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, scale, om, lse_ptr, workspace.data_ptr(), ws_bytes,
+                        torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(st, "attn_paged")
     return out if lse is None else (out, lse)
 
 
@@ -508,22 +510,25 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
     Returns out, a new tensor unless given; out=weights adds in place. workspace
     as for attn_paged."""
     import torch
+    dev, rows = cache.device, batch * t_q
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return attn_paged_weights(q, cache, lse, batch, t_q, n_heads, window, first, causal, q_lens, scale, weights,
+                                      out, workspace)
     lib = load_library()
     kv = _batch_of(cache, batch)
-    dev, rows = cache.device, batch * t_q
     qm = _rows(q, "q", rows, n_heads * HEAD_DIM, dev)
     mask = AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, dev))
     lse_ptr = _dev_tensor(lse, "lse", torch.float32, (rows, n_heads), dev)
     shape = (batch, cache.slots)
     w_in = 0 if weights is None else _dev_tensor(weights, "weights", torch.float32, shape, dev)
-    with _On(dev, stream) as s:
-        if out is None:
-            out = lse.new_empty(shape)
-        w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
-        workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
-        st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out,
-                                    workspace.data_ptr(), ws_bytes, s)
-        _check(st, "attn_paged_weights")
+    if out is None:
+        out = lse.new_empty(shape)
+    w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
+    workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
+    st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out, workspace.data_ptr(),
+                                ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(st, "attn_paged_weights")
     return out
 
 
@@ -537,23 +542,25 @@ def attn_paged_evict(cache: PagedKV, weights, budget, first=0, recent=0, dst: Op
     dst.lens is written. Without weights_out a new tensor is returned;
     weights_out=weights works in place when dst has as many slots."""
     import torch
-    lib = load_library()
     batch, dev = cache.batch, cache.device
+    if _elsewhere(torch, dev, stream):
+        with _on(dev, stream):
+            return attn_paged_evict(cache, weights, budget, first, recent, dst, kept, weights_out)
     if dst is None:
         dst = cache
-    if dst.device != dev:
+    elif dst.device != dev:
         raise ValueError(f"dst is on {dst.device}, the cache on {dev}")
     to = _batch_of(dst, batch)
     w_in = _dev_tensor(weights, "weights", torch.float32, (batch, cache.slots), dev)
-    with _On(dev, stream) as s:
-        if kept is None:
-            kept = weights.new_empty((batch, budget), dtype=torch.int32)
-        if weights_out is None:
-            weights_out = weights.new_empty((batch, dst.slots))
-        st = lib.attn_paged_evict(cache.c, batch, budget, first, recent, w_in, to,
-                                  _dev_tensor(weights_out, "weights_out", torch.float32, (batch, dst.slots), dev),
-                                  _dev_tensor(kept, "kept", torch.int32, (batch, budget), dev), s)
-        _check(st, "attn_paged_evict")
+    if kept is None:
+        kept = weights.new_empty((batch, budget), dtype=torch.int32)
+    if weights_out is None:
+        weights_out = weights.new_empty((batch, dst.slots))
+    w_out = _dev_tensor(weights_out, "weights_out", torch.float32, (batch, dst.slots), dev)
+    st = load_library().attn_paged_evict(cache.c, batch, budget, first, recent, w_in, to, w_out,
+                                         _dev_tensor(kept, "kept", torch.int32, (batch, budget), dev),
+                                         torch._C._cuda_getCurrentRawStream(dev.index))
+    _check(st, "attn_paged_evict")
     return kept, weights_out
 
 
