@@ -169,7 +169,10 @@ __device__ __forceinline__ void walk_cut(const Geo& g, Walk& w, int k0) {
 // One warp; returns false if the part is empty.
 __device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int part, int parts, int least) {
   const int lane = threadIdx.x & 31;
-  const long long total = tiles_before(g, g.batch);
+  // Up to 32 sequences: a lane each, looked at once.
+  const bool once = g.q_tiles <= 4 && g.batch <= 32;
+  const int lane_tiles = once && lane < g.batch ? tiles_of_seq(g, lane) : 0;
+  const long long total = once ? __reduce_add_sync(0xffffffffu, lane_tiles) : tiles_before(g, g.batch);
   const long long per = share_of(total, parts, least);
   w.begin = w.pos = per * part;
   w.end = min(total, w.pos + per);
@@ -179,7 +182,7 @@ __device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int part, int 
   int b = 0;
   if (g.q_tiles <= 4) {
     for (int b0 = 0; b0 < g.batch; b0 += 32) {
-      const int n = b0 + lane < g.batch ? tiles_of_seq(g, b0 + lane) : 0;
+      const int n = once ? lane_tiles : b0 + lane < g.batch ? tiles_of_seq(g, b0 + lane) : 0;
       long long incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {

@@ -261,6 +261,7 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   // Rows of a query tile: as few as hold the chunk, a whole number of tokens.
   const int n = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : 128;
   p.g.tok_per_tile = static_cast<int>(std::min<int64_t>(t_q, n / p.g.group));
+  p.g.q_tiles = ceil_div(t_q, p.g.tok_per_tile);
   p.dv_group = make_divc(p.g.group);
   p.lse = lse;
   p.w_in = w_in;

@@ -171,6 +171,41 @@ __device__ __forceinline__ void locate(const WeightParams& p, int cta, int ctas,
                                        Located* found) {
   const Geo& g = p.g;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (g.q_tiles == 1) {
+    // One query tile: the key tiles of a sequence are those of its span, with
+    // as many items each as there are K/V heads. One warp places the share.
+    if (warp == 0) {
+      const long long total = tiles_before(g, g.batch) * g.kv_heads;
+      const long long per = (total + ctas - 1) / ctas;
+      const long long pos = per * cta;
+      if (lane == 0) {
+        found->per = per;
+        found->left = max(0ll, min(per, total - pos));
+      }
+      long long base = 0;
+      for (int b0 = 0; b0 < g.batch && base <= pos && pos < total; b0 += 32) {
+        Span u{};
+        if (b0 + lane < g.batch) u = span_of(g, seq_of(g, b0 + lane), 0);
+        const long long mine = static_cast<long long>(u.n) * g.kv_heads;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const long long before = base + incl - mine;
+        if (pos >= before && pos < before + mine) {
+          const int k = static_cast<int>((pos - before) / g.kv_heads);
+          found->b = b0 + lane;
+          found->tile = u.tile(k);
+          found->i0 = static_cast<int>(pos - before - static_cast<long long>(k) * g.kv_heads);
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const int entries = g.batch * p.tiles;
   const int run = (entries + threads - 1) / threads;
   const int a = min(entries, t * run), z = min(entries, a + run);
