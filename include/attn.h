@@ -319,17 +319,19 @@ attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cach
  * A row that sees nothing (padding rows i >= Q too) is zero with lse = -inf.
  * Precision as in attn_forward: fp32 scores, max, sum and output, softmax
  * weights rounded to fp16 for the value product, the output rounded once.
- * workspace: at least attn_paged_workspace_size(...) bytes, 16-byte aligned;
- * NULL or a smaller one returns ATTN_ERR_INVALID. Calls that may run at the
- * same time need a workspace each. The result does not depend on timing.
+ * workspace: at least attn_paged_workspace_size(...) bytes, 16-byte aligned
+ * (NULL with 0 bytes where that is 0: short caches and windows); a smaller one
+ * returns ATTN_ERR_INVALID. Calls that may run at the same time need a
+ * workspace each. The result does not depend on timing.
  */
 attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                        attn_paged_mask mask, const float *sinks, float scale, attn_mat out, float *lse,
                        void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
-/* Bytes of workspace attn_paged and attn_paged_weights need for these sizes on the current device (0 for
-   invalid sizes). */
-size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, int32_t n_kv_heads);
+/* Bytes of workspace attn_paged needs for these arguments on the current device (0 for none, and for invalid
+   arguments). It depends on sizes, window, first and causal, not on what table and lengths hold. */
+size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                                 attn_paged_mask mask);
 
 /*
  * attn_paged_weights -- the attention weight each slot receives from a chunk
@@ -339,11 +341,16 @@ size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, in
  *   lse    [batch*t_q, n_heads] fp32
  *   w_in   [batch, pages_per_seq*page_size] fp32, or NULL for zeros
  *   w_out  the same shape; w_in itself, or not overlapping it
- * workspace: as for attn_paged.
+ * workspace: at least attn_paged_weights_workspace_size() bytes, 16-byte
+ * aligned; NULL or a smaller one returns ATTN_ERR_INVALID. Calls that may run at
+ * the same time need a workspace each.
  */
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                attn_paged_mask mask, const float *lse, float scale, const float *w_in, float *w_out,
                                void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* Bytes of workspace attn_paged_weights needs on the current device, whatever the sizes (0 without a device). */
+size_t attn_paged_weights_workspace_size(void);
 
 /*
  * attn_paged_evict -- shrinks each sequence to at most `budget` slots

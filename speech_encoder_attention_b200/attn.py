@@ -128,7 +128,9 @@ SIGNATURES = {
     "attn_paged": (ctypes.c_int, [AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, AttnPagedMask,
                                   ctypes.c_void_p, ctypes.c_float, AttnMat, ctypes.c_void_p, ctypes.c_void_p,
                                   ctypes.c_size_t, ctypes.c_void_p]),
-    "attn_paged_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "attn_paged_workspace_size": (ctypes.c_size_t, [AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                    AttnPagedMask]),
+    "attn_paged_weights_workspace_size": (ctypes.c_size_t, []),
     "attn_paged_weights": (ctypes.c_int, [AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                           AttnPagedMask, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
@@ -451,18 +453,24 @@ def attn_paged_append(k_new, v_new, cache: PagedKV, batch, t_new, q_lens=None, s
     _check(st, "attn_paged_append")
 
 
-def paged_workspace_size(batch, t_q, n_heads, n_kv_heads) -> int:
-    return int(load_library().attn_paged_workspace_size(batch, t_q, n_heads, n_kv_heads))
+def paged_workspace_size(cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal=True) -> int:
+    """Bytes of workspace attn_paged needs for these sizes on the current device."""
+    mask = AttnPagedMask(window, first, 1 if causal else 0, 0)
+    return int(load_library().attn_paged_workspace_size(_batch_of(cache, batch), batch, t_q, n_heads, mask))
 
 
-def _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads):
-    if workspace is None:
-        import torch
-        nbytes = lib.attn_paged_workspace_size(batch, t_q, n_heads, cache.n_kv_heads)
-        return q.new_empty(nbytes, dtype=torch.uint8), nbytes
-    if workspace.device != cache.device:
-        raise ValueError(f"workspace is on {workspace.device}, the cache on {cache.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+def paged_weights_workspace_size() -> int:
+    """Bytes of workspace attn_paged_weights needs on the current device."""
+    return int(load_library().attn_paged_weights_workspace_size())
+
+
+def _given_workspace(workspace, device):
+    """A caller's workspace as (pointer, bytes)."""
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the cache on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal=True, q_lens=None, sinks=None,
@@ -472,7 +480,7 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
     sees to the last `window` slots and the `first` first ones (window=0: all).
     Returns out, or (out, lse) with return_lse or lse given; lse is
     [batch*t_q, n_heads] fp32, the log of each row's softmax denominator.
-    Without workspace one is allocated for the call."""
+    Without workspace one is allocated for the call, if it needs any."""
     import torch
     dev, rows, cols = cache.device, batch * t_q, n_heads * HEAD_DIM
     if _elsewhere(torch, dev, stream):
@@ -496,8 +504,14 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
         lse_ptr = lse.data_ptr()
     else:
         lse_ptr = 0
-    workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
-    st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, scale, om, lse_ptr, workspace.data_ptr(), ws_bytes,
+    if workspace is not None:
+        ws_ptr, ws_bytes = _given_workspace(workspace, dev)
+    else:
+        ws_ptr, ws_bytes = 0, lib.attn_paged_workspace_size(kv, batch, t_q, n_heads, mask)
+        if ws_bytes:
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+            ws_ptr = workspace.data_ptr()
+    st = lib.attn_paged(qm, kv, batch, t_q, n_heads, mask, sinks_ptr, scale, om, lse_ptr, ws_ptr, ws_bytes,
                         torch._C._cuda_getCurrentRawStream(dev.index))
     _check(st, "attn_paged")
     return out if lse is None else (out, lse)
@@ -507,8 +521,8 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
                        scale=DEFAULT_SCALE, weights=None, out=None, workspace=None, stream=None):
     """What attn_paged's rows put on each slot, summed over rows and heads, added
     to weights ([batch, cache.slots] fp32; None: zeros). lse is attn_paged's.
-    Returns out, a new tensor unless given; out=weights adds in place. workspace
-    as for attn_paged."""
+    Returns out, a new tensor unless given; out=weights adds in place. Without
+    workspace one is allocated for the call."""
     import torch
     dev, rows = cache.device, batch * t_q
     if _elsewhere(torch, dev, stream):
@@ -525,9 +539,11 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
     if out is None:
         out = lse.new_empty(shape)
     w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
-    workspace, ws_bytes = _paged_workspace(lib, workspace, q, cache, batch, t_q, n_heads)
-    st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out, workspace.data_ptr(),
-                                ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    if workspace is None:
+        workspace = lse.new_empty(lib.attn_paged_weights_workspace_size(), dtype=torch.uint8)
+    ws_ptr, ws_bytes = _given_workspace(workspace, dev)
+    st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out, ws_ptr, ws_bytes,
+                                torch._C._cuda_getCurrentRawStream(dev.index))
     _check(st, "attn_paged_weights")
     return out
 

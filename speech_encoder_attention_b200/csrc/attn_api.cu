@@ -694,11 +694,20 @@ attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t
   return launch_paged(q, cache, batch, t_q, n_heads, mask, sinks, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
-size_t attn_paged_workspace_size(int32_t batch, int32_t t_q, int32_t n_heads, int32_t n_kv_heads) {
-  if (!valid_paged_heads(batch, t_q, n_heads, n_kv_heads)) return 0;
+size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                                 attn_paged_mask mask) {
+  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch) ||
+      !valid_paged_mask(mask))
+    return 0;
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != ATTN_OK) return 0;
-  return plan_paged(t_q, n_heads, n_kv_heads, dev->num_sms).ws_bytes;
+  return plan_paged(paged_geo(cache, batch, t_q, n_heads, mask), dev->num_sms).ws_bytes;
+}
+
+size_t attn_paged_weights_workspace_size(void) {
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev) != ATTN_OK) return 0;
+  return paged_weights_workspace(sea::pg::WeightCfg<16>::CTAS_PER_SM * dev->num_sms);
 }
 
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,

@@ -94,19 +94,6 @@ __device__ __forceinline__ bool chunk_next(const ChunkParams& p, ChunkWalk& w) {
   return true;
 }
 
-// One warp: the rows of a query tile that sees nothing.
-__device__ __forceinline__ void zero_rows(const StepParams& p, int b, int h, int tok0) {
-  const Geo& g = p.g;
-  const int rows = min(g.tok_per_tile, g.t_q - tok0) * g.group;
-  for (int x = threadIdx.x & 31; x < rows * 8; x += 32) {
-    const int r = x >> 3;
-    const int64_t row = static_cast<int64_t>(b) * g.t_q + tok0 + r / g.group;
-    const int head = h * g.group + r % g.group;
-    reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * DH)[x & 7] = make_uint4(0u, 0u, 0u, 0u);
-    if (p.lse != nullptr && (x & 7) == 0) p.lse[row * g.n_heads + head] = -INFINITY;
-  }
-}
-
 __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const ChunkParams cp) {
@@ -179,7 +166,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
     bool more = chunk_start(cp, w), ok = true;
     for (; more; more = ok && chunk_next(cp, w)) {
       if (w.k1 <= w.k0) {  // no row sees anything (whole units only)
-        zero_rows(p, w.b, w.h, w.u.tok0);
+        zero_rows(p, w.b, w.h, w.u.tok0, min(w.u.tok0 + g.tok_per_tile, g.t_q));
         continue;
       }
       const int qb = qn & 1;

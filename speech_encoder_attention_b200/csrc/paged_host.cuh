@@ -105,15 +105,19 @@ bool encode_paged_q(CUtensorMap* m, const attn_mat& q, int batch, int t_q, int n
 // Chunks with at least this many units per CTA are walked unit by unit.
 constexpr int kWholeUnitsPerCta = 4;
 
+// A unit of paged_step_kernel with at most this many key tiles gets a CTA of
+// its own instead of being cut into parts.
+constexpr int kWholeStepTiles = 12;
+
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
   int tok_per_tile, q_tiles;
-  int parts, ctas;    // CTAs: one per part and K/V head
+  int parts, ctas;    // CTAs: one per part and K/V head; parts 0: one per unit
   size_t ws_bytes;
 };
 
-PagedPlan plan_paged(int t_q, int n_heads, int kv_heads, int num_sms) {
-  const int group = n_heads / kv_heads;
+PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
+  const int t_q = g.t_q, kv_heads = g.kv_heads, group = g.group;
   PagedPlan pl{};
   // Up to 32 rows per K/V head: paged_step_kernel with 16 or 32 rows per tile.
   const int64_t rows = static_cast<int64_t>(t_q) * group;
@@ -122,6 +126,20 @@ PagedPlan plan_paged(int t_q, int n_heads, int kv_heads, int num_sms) {
   pl.q_tiles = ceil_div(t_q, pl.tok_per_tile);
   pl.parts = std::max(1, 2 * num_sms / kv_heads);
   pl.ctas = pl.parts * kv_heads;
+  if (pl.rows_cap <= 32) {
+    // The cache bounds a unit's key tiles, or the window (its other side too
+    // unless causal), whose ends fall inside tiles, and the first tokens.
+    int64_t tiles = ceil_div(g.cap, sea::pg::BKV);
+    if (g.window > 0) {
+      const int64_t reach = int64_t(g.causal ? 1 : 2) * g.window + t_q;
+      tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
+    }
+    if (tiles <= kWholeStepTiles) {
+      pl.parts = 0;
+      pl.ctas = g.batch * kv_heads;
+      return pl;
+    }
+  }
   pl.ws_bytes = size_t(2) * pl.ctas * pl.rows_cap * (sea::pg::DH * sizeof(float) + sizeof(float2));
   return pl;
 }
@@ -173,19 +191,19 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   if (overlaps(ro, mat_range(q.ptr, rows, cols, q.row_stride)) || overlaps(ro, pool_range(cache, cache.k)) ||
       overlaps(ro, pool_range(cache, cache.v)))
     return ATTN_ERR_INVALID;
-  if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_INVALID;
+  if (!aligned16(workspace) || (workspace == nullptr && workspace_bytes != 0)) return ATTN_ERR_INVALID;
 
   DeviceInfo* dev = nullptr;
   if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
-  const PagedPlan pl = plan_paged(t_q, n_heads, cache.n_kv_heads, dev->num_sms);
+  sea::pg::StepParams p{};
+  p.g = paged_geo(cache, batch, t_q, n_heads, mask);
+  const PagedPlan pl = plan_paged(p.g, dev->num_sms);
   if (workspace_bytes < pl.ws_bytes) return ATTN_ERR_INVALID;
   const int64_t units = static_cast<int64_t>(batch) * cache.n_kv_heads * pl.q_tiles;
   if (units > INT32_MAX) return ATTN_ERR_INVALID;
 
   CUtensorMap tk, tv;
   if (!encode_pages(&tk, cache, cache.k) || !encode_pages(&tv, cache, cache.v)) return ATTN_ERR_CUDA;
-  sea::pg::StepParams p{};
-  p.g = paged_geo(cache, batch, t_q, n_heads, mask);
   p.g.tok_per_tile = pl.tok_per_tile;
   p.g.q_tiles = pl.q_tiles;
   p.q = static_cast<const __half*>(q.ptr);
@@ -225,6 +243,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
                                          StepCfg<2>::SMEM_BYTES, stream, tk, tv, p);
   }
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
+  if (pl.parts == 0) return ATTN_OK;
   const int unit_rows = pl.tok_per_tile * p.g.group;
   const int rows_log2 = log2_of(std::min(unit_rows, 32));
   if (launch_pdl(sea::pg::paged_combine_kernel,
@@ -233,6 +252,9 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }
+
+// Sums and states of the CTAs of paged_weights_kernel, at most four per SM.
+size_t paged_weights_workspace(int ctas) { return size_t(ctas) * (2 * sea::pg::BKV + 3) * 4; }
 
 attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                  attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
@@ -279,7 +301,7 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   auto launch = [&](auto kernel, auto cfg) -> attn_status {
     using C = decltype(cfg);
     const int ctas = C::CTAS_PER_SM * dev->num_sms;
-    if (workspace_bytes < size_t(ctas) * (2 * sea::pg::BKV + 3) * 4) return ATTN_ERR_INVALID;
+    if (workspace_bytes < paged_weights_workspace(ctas)) return ATTN_ERR_INVALID;
     p.ws_sum = static_cast<float*>(workspace);
     p.ws_state = reinterpret_cast<int*>(p.ws_sum + size_t(ctas) * 2 * sea::pg::BKV);
     if (launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::SMEM_BYTES, stream, tq, tk, p) != cudaSuccess ||

@@ -17,7 +17,8 @@
 //               four at the end of a unit.
 // The key tiles of all units are cut into equal parts, a CTA for each part and
 // K/V head, two CTAs per SM; units that are cut leave partials that
-// paged_combine_kernel merges.
+// paged_combine_kernel merges. Where a unit has few key tiles at most, a CTA per
+// unit (and no second launch) takes less time than cutting and merging.
 #pragma once
 
 #include "paged_common.cuh"
@@ -41,7 +42,7 @@ struct StepParams {
   float* ws_o;       // [2 * CTAs][rows_cap][64] unnormalised partial O
   float2* ws_ml;     // [2 * CTAs][rows_cap] (m in log2 units, l)
   int rows_cap;
-  int parts;         // the line of key tiles is cut into this many
+  int parts;         // the line of key tiles is cut into this many; 0: a CTA per unit
   int least;         // fewest key tiles per part
   uint32_t* err;
   uint64_t limit_ns;
@@ -86,6 +87,18 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// One warp: the rows of tokens [tok_a, tok_z) of one K/V head see nothing.
+__device__ __forceinline__ void zero_rows(const StepParams& p, int b, int h, int tok_a, int tok_z) {
+  const Geo& g = p.g;
+  for (int x = threadIdx.x & 31; x < (tok_z - tok_a) * g.group * 8; x += 32) {
+    const int r = x >> 3;
+    const int64_t row = static_cast<int64_t>(b) * g.t_q + tok_a + r / g.group;
+    const int head = h * g.group + r % g.group;
+    reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * DH)[x & 7] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse != nullptr && (x & 7) == 0) p.lse[row * g.n_heads + head] = -INFINITY;
+  }
+}
+
 template <int MT>
 __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
     paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -123,7 +136,23 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
 
   const int h = blockIdx.x % g.kv_heads;
   Walk w;
-  const bool any = walk_start(g, w, blockIdx.x / g.kv_heads, p.parts, p.least);
+  bool any;
+  if (p.parts > 0) {
+    any = walk_start(g, w, blockIdx.x / g.kv_heads, p.parts, p.least);
+  } else {
+    w.b = blockIdx.x / g.kv_heads;
+    w.qt = 0;
+    w.s = seq_of(g, w.b);
+    w.u = span_of(g, w.s, 0);
+    w.k0 = 0;
+    w.k1 = w.u.n;
+    w.whole = true;
+    any = w.u.n > 0;
+    // rows that see nothing: all of them, or the padding behind the valid ones
+    if (warp == 0) zero_rows(p, w.b, h, w.u.tok0 + (any ? w.u.ntok : 0), g.t_q);
+  }
+  // the next unit of this CTA
+  auto next_unit = [&]() { return p.parts > 0 && walk_next(g, w); };
   if (any && warp == C::WARPS) {
     // ---------------- producer ----------------
     const int n_pages = pages_per_tile(g);
@@ -149,7 +178,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
           tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, full(st), h * DH, l.row);
         }
       }
-    } while (ok && walk_next(g, w));
+    } while (ok && next_unit());
     // Let the last copies land before the CTA may exit.
     for (int i = max(0, it - ST); i < it; ++i) mbar_wait_drain(full(i % ST), (i / ST) & 1, p.limit_ns);
   } else if (any) {
@@ -394,7 +423,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
         if (lane == 0) mbar_arrive(merge_empty);
       }
       ++unit;
-    } while (walk_next(g, w));
+    } while (next_unit());
   }
   __syncthreads();
 }

@@ -60,10 +60,10 @@ CASES = {
 }
 
 
-def inputs(name):
+def inputs(name, slots=None):
     c = CASES[name]
     rng = np.random.default_rng(sum(map(ord, name)))
-    cache = make_cache(rng, c["lens"], c["kv"], c["page"], holes=c.get("holes", ()), garbage=NAN,
+    cache = make_cache(rng, c["lens"], c["kv"], c["page"], slots=slots, holes=c.get("holes", ()), garbage=NAN,
                        packed=len(name) % 2 == 0)
     batch = len(c["lens"])
     q = queries(rng, batch, c["t_q"], c["heads"], wide=64)
@@ -76,9 +76,11 @@ def inputs(name):
     return c, rng, cache, batch, q, opts, q_lens, sinks
 
 
+# With few slots per sequence a CTA walks a whole unit; with many the units may be cut.
+@pytest.mark.parametrize("slots", [None, 5000])
 @pytest.mark.parametrize("name", CASES)
-def test_attention_matches_the_oracle(name):
-    c, _, cache, batch, q, opts, q_lens, sinks = inputs(name)
+def test_attention_matches_the_oracle(name, slots):
+    c, _, cache, batch, q, opts, q_lens, sinks = inputs(name, slots)
     out = torch.full((batch * c["t_q"], c["heads"] * 64 + 8), 7.0, dtype=torch.float16, device="cuda")
     got, lse = attn.attn_paged(q, cache, batch, c["t_q"], c["heads"], q_lens=i32(q_lens), sinks=sinks, out=out,
                                return_lse=True, **opts)
@@ -126,6 +128,8 @@ LARGE = {
     "chunk_open": dict(lens=[1000, 640], t_q=300, heads=6, kv=6, page=16, causal=False),
     "window_step": dict(lens=[16000, 9000, 300], t_q=1, heads=20, kv=5, page=32, window=1024, first=4),
     "many": dict(lens=[5 + 37 * i % 400 for i in range(70)], t_q=2, heads=8, kv=4, page=16),
+    "prompt_many": dict(lens=[max(i % 7 * 50, i * 37 % 300) for i in range(31)], t_q=200, heads=20, kv=20, page=64,
+                        q_lens=[min(200, max(i % 7 * 50, i * 37 % 300)) for i in range(31)]),
     "chunk_many": dict(lens=[150 + 37 * i % 400 for i in range(40)], t_q=140, heads=2, kv=1, page=16),
 }
 
@@ -299,16 +303,17 @@ def test_a_decode_loop_with_eviction():
     assert evicted >= 1
 
 
-def test_captured_step_follows_its_inputs():
+@pytest.mark.parametrize("slots", [400, 4000])
+def test_captured_step_follows_its_inputs(slots):
     """One captured decode step replayed while lengths, pages and rows change."""
     rng = np.random.default_rng(12)
     batch, heads, page = 3, 4, 16
-    cache = make_cache(rng, [400, 400, 400], 4, page)
+    cache = make_cache(rng, [400, 400, 400], 4, page, slots=slots)
     q = queries(rng, batch, 1, heads)
     w = torch.zeros(batch, cache.slots, device="cuda")
     out = torch.empty(batch, heads * 64, dtype=torch.float16, device="cuda")
     lse = torch.empty(batch, heads, device="cuda")
-    ws = torch.empty(attn.paged_workspace_size(batch, 1, heads, 4), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(attn.paged_workspace_size(cache, batch, 1, heads), dtype=torch.uint8, device="cuda")
 
     def step():
         attn.attn_paged_append(q, q, cache, batch, 1)
@@ -389,8 +394,10 @@ def test_another_device_and_stream_are_refused_or_followed():
         attn.attn_paged(q, cache, 1, 2, 2)
     with pytest.raises(ValueError):
         attn.attn_paged(q, cache, 2, 1, 2)
+    long = make_cache(rng, [90], 2, 16, slots=9000)
+    assert attn.paged_workspace_size(cache, 1, 1, 2) == 0 < attn.paged_workspace_size(long, 1, 1, 2)
     with pytest.raises(attn.AttnError):
-        attn.attn_paged(q, cache, 1, 1, 2, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        attn.attn_paged(q, long, 1, 1, 2, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
 
 
 @pytest.mark.parametrize("t_q", [1, 12, 40])

@@ -57,7 +57,7 @@ def test_every_entry_rejects_a_bad_cache(lib, kw):
     dict(batch=0), dict(batch=70000), dict(t_q=0), dict(heads=0), dict(heads=3), dict(heads=2 * 129),
     dict(q=m(0, 256)), dict(q=m(Q, 248)), dict(q=m(Q + 8, 256)), dict(out=m(OUT, 128)), dict(out=m(Q + 64, 256)),
     dict(out=m(KP, 256)), dict(out=m(VP + 128, 256)), dict(scale=0.0), dict(scale=float("nan")),
-    dict(scale=float("inf")), dict(sinks=LSE + 2), dict(lse=LSE + 1), dict(ws=0), dict(ws=WS + 8),
+    dict(scale=float("inf")), dict(sinks=LSE + 2), dict(lse=LSE + 1), dict(ws=0), dict(ws=WS + 8), dict(ws=0, ws_bytes=16),
     dict(mk=mask(window=-1)), dict(mk=mask(first=2)), dict(mk=mask(window=4, first=-1)), dict(mk=mask(causal=2)),
     dict(mk=mask(q_lens=LSE + 2)),
 ])
@@ -109,10 +109,10 @@ def test_evict_rejects_invalid_arguments(lib, kw):
 
 
 def test_workspace_size_of_invalid_sizes_is_zero(lib):
-    assert lib.attn_paged_workspace_size(0, 1, 4, 4) == 0
-    assert lib.attn_paged_workspace_size(1, 0, 4, 4) == 0
-    assert lib.attn_paged_workspace_size(1, 1, 4, 3) == 0
-    assert lib.attn_paged_workspace_size(1, 1, 129, 1) == 0
+    assert lib.attn_paged_workspace_size(cache(), 0, 1, 4, mask()) == 0
+    assert lib.attn_paged_workspace_size(cache(), 1, 0, 4, mask()) == 0
+    assert lib.attn_paged_workspace_size(cache(n_kv_heads=3), 1, 1, 4, mask()) == 0
+    assert lib.attn_paged_workspace_size(cache(n_kv_heads=1), 1, 1, 129, mask()) == 0
 
 
 def test_binding_refuses_bad_caches():
