@@ -65,24 +65,23 @@ struct StepCfg {
   static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 8;
 };
 
+// volatile keeps these between the waits on the tile's barriers; without a
+// memory clobber the arithmetic may move around them.
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -275,40 +274,55 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
             }
           }
         }
+        // A row's reference moves only when one of its scores would pass 2^15;
+        // whether any does takes one vote, and the row's max (two shuffles) only
+        // then.
+        float top[MT][2];
+        bool passes = false;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = fmax3(s[m][0][2 * e], s[m][0][2 * e + 1], s[m][1][2 * e]);
+            const float c = fmax3(s[m][1][2 * e + 1], s[m][2][2 * e], s[m][2][2 * e + 1]);
+            top[m][e] = fmaxf(fmax3(a, c, s[m][3][2 * e]), s[m][3][2 * e + 1]) * sl2;
+            passes |= top[m][e] > m_run[m][e] + RESCALE_LIMIT;
+          }
+        if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(top[m][e], __shfl_xor_sync(0xffffffffu, top[m][e], 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              if (mx > m_run[m][e] + RESCALE_LIMIT) {  // the same in the row's four threads
+                const float alpha = ex2_approx(m_run[m][e] - mx);
+                l_run[m][e] *= alpha;
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {
+                  o[m][d][2 * e] *= alpha;
+                  o[m][d][2 * e + 1] *= alpha;
+                }
+                m_run[m][e] = mx;
+              }
+            }
+        }
         uint32_t pf[MT][2][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) mx = fmax3(mx, s[m][n][2 * e], s[m][n][2 * e + 1]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mx2 = mx * sl2;
-            const bool grow = mx2 > m_run[m][e] + RESCALE_LIMIT;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float m_new = grow ? mx2 : m_run[m][e];
-              const float alpha = grow ? ex2_approx(m_run[m][e] - m_new) : 1.f;
-              l_run[m][e] *= alpha;
-#pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                o[m][d][2 * e] *= alpha;
-                o[m][d][2 * e + 1] *= alpha;
-              }
-              m_run[m][e] = m_new;
-            }
             const float ref = m_run[m][e] == -INFINITY ? 0.f : m_run[m][e];
-            float sum = 0.f;
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
               const float p0 = ex2_approx(fmaf(s[m][n][2 * e], sl2, -ref));
               const float p1 = ex2_approx(fmaf(s[m][n][2 * e + 1], sl2, -ref));
-              sum += p0 + p1;
+              sum[n & 1] += p0 + p1;
               // P is rounded to fp16 for the tensor cores; the sum is not
               pf[m][n >> 1][(n & 1) * 2 + e] = pack_half2(p0, p1);
             }
-            l_run[m][e] += sum;
+            l_run[m][e] += sum[0] + sum[1];
           }
         }
         // O += P V
