@@ -23,6 +23,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 from collections import namedtuple
 from typing import Optional
@@ -371,21 +372,40 @@ class PagedKV(namedtuple("PagedKV", "k v table lens page_size n_kv_heads batch s
         import torch
         if page_size not in (16, 32, 64, 128, 256):
             raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, got {page_size}")
-        km, vm = _mat(k), _mat(v)
-        dev = k.device
-        (rows, k_cols), (v_rows, v_cols) = k.shape, v.shape
+        if n_kv_heads < 1:
+            raise ValueError("n_kv_heads must be positive")
         cols = n_kv_heads * HEAD_DIM
+        (k_ptr, rows, k_stride), (v_ptr, v_rows, v_stride) = _half_rows(k, "k", cols), _half_rows(v, "v", cols)
+        dev = k.device
         if v.device != dev or v_rows != rows:
             raise ValueError("the K and V pools must lie on one device and have as many rows")
-        if rows == 0 or rows % page_size or n_kv_heads < 1 or k_cols < cols or v_cols < cols:
-            raise ValueError(f"the pools must hold whole pages of {page_size} rows of {cols} columns")
-        if table.dim() != 2:
+        if rows == 0 or rows % page_size:
+            raise ValueError(f"the pools must hold whole pages of {page_size} rows")
+        shape = table.shape
+        if len(shape) != 2:
             raise ValueError("table must be a [batch, pages_per_seq] int32 tensor")
-        batch, per_seq = table.shape
-        c = AttnPagedKV(km, vm, _dev_tensor(table, "table", torch.int32, (batch, per_seq), dev),
-                        _dev_tensor(lens, "lens", torch.int32, (batch,), dev), rows // page_size, page_size, per_seq,
-                        n_kv_heads)
+        batch, per_seq = shape
+        table_ptr = _dev_tensor(table, "table", torch.int32, shape, dev)
+        lens_ptr = _dev_tensor(lens, "lens", torch.int32, (batch,), dev)
+        c = AttnPagedKV.from_buffer_copy(_PAGED_KV.pack(k_ptr, k_stride, v_ptr, v_stride, table_ptr, lens_ptr,
+                                                        rows // page_size, page_size, per_seq, n_kv_heads))
         return tuple.__new__(cls, (k, v, table, lens, page_size, n_kv_heads, batch, per_seq * page_size, dev, c))
+
+
+_PAGED_KV = struct.Struct("@QqQqQQiiii")  # the fields of AttnPagedKV, in order
+
+
+def _half_rows(t, what: str, cols: int):
+    """(pointer, rows, row stride) of a 2-D CUDA fp16 tensor of at least cols columns, or a column view of one."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype is not torch.float16:
+        raise ValueError(f"{what} must be float16, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] < cols or stride[1] != 1:
+        raise ValueError(f"{what} must be 2-D with unit column stride and at least {cols} columns, got {list(shape)}")
+    return t.data_ptr(), shape[0], stride[0]
 
 
 def _dev_tensor(t, what: str, dtype, shape, device) -> int:
@@ -397,13 +417,12 @@ def _dev_tensor(t, what: str, dtype, shape, device) -> int:
 
 
 def _rows(t, what: str, rows: int, cols: int, device) -> AttnMat:
-    m = _mat(t)
+    ptr, have, stride = _half_rows(t, what, cols)
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the cache on {device}")
-    have, wide = t.shape
-    if have != rows or wide < cols:
-        raise ValueError(f"{what} must have {rows} rows of at least {cols} columns, got [{have}, {wide}]")
-    return m
+    if have != rows:
+        raise ValueError(f"{what} must have {rows} rows, got {have}")
+    return AttnMat(ptr, stride)
 
 
 def _batch_of(cache: PagedKV, batch: int) -> AttnPagedKV:

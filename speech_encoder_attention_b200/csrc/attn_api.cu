@@ -104,6 +104,15 @@ auto narrow_attention_kernel(bool ext) {
   return ext ? sea::fa::flash_attn_kernel<false, true, 4, true> : sea::fa::flash_attn_kernel<false, false, 4, true>;
 }
 
+template <int MT>
+bool set_paged_step_smem() {
+  constexpr int bytes = sea::pg::StepCfg<MT>::SMEM_BYTES;
+  return cudaFuncSetAttribute(sea::pg::paged_step_kernel<MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              bytes) == cudaSuccess &&
+         cudaFuncSetAttribute(sea::pg::paged_step_kernel<MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              bytes) == cudaSuccess;
+}
+
 // Per-device set-up: checks for an sm_100 part, records the SM count and the
 // error-word address, and raises the dynamic shared-memory limits once.
 attn_status device_info(DeviceInfo** out) {
@@ -132,10 +141,7 @@ attn_status device_info(DeviceInfo** out) {
                              sea::gemm::PairShape::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::q8::qkv_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::q8::SMEM_BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(sea::pg::paged_step_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sea::pg::StepCfg<1>::SMEM_BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(sea::pg::paged_step_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sea::pg::StepCfg<2>::SMEM_BYTES) != cudaSuccess ||
+        !set_paged_step_smem<1>() || !set_paged_step_smem<2>() ||
         cudaFuncSetAttribute(sea::pg::paged_weights_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::pg::WeightCfg<16>::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::pg::paged_weights_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -105,14 +105,19 @@ bool encode_paged_q(CUtensorMap* m, const attn_mat& q, int batch, int t_q, int n
 // Chunks with at least this many units per CTA are walked unit by unit.
 constexpr int kWholeUnitsPerCta = 4;
 
-// A unit of paged_step_kernel with at most this many key tiles gets a CTA of
-// its own instead of being cut into parts.
-constexpr int kWholeStepTiles = 12;
+// A unit of paged_step_kernel gets a cluster of its own instead of being cut into
+// parts where a CTA of it has at most kClusterStepTiles key tiles, and a single CTA
+// up to kCtaStepTiles. One token, 20 heads, us per step: a CTA 4.5 at 128 slots,
+// 6.5 at 448, 7.8 at 768, 11.9 at 1500; a cluster of eight 7.6 at 1500, 8.2 at
+// 3000, 17.1 at 12000; cut parts 10.3 at 448, 12.2 at 3000, 19.6 at 12000.
+constexpr int kCtaStepTiles = 6;
+constexpr int kClusterStepTiles = 12;
 
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
   int tok_per_tile, q_tiles;
-  int parts, ctas;    // CTAs: one per part and K/V head; parts 0: one per unit
+  int parts, ctas;    // CTAs: one per part and K/V head, or (parts 0)
+  int cluster;        // so many per unit
   size_t ws_bytes;
 };
 
@@ -134,9 +139,14 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
       const int64_t reach = int64_t(g.causal ? 1 : 2) * g.window + t_q;
       tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
     }
-    if (tiles <= kWholeStepTiles) {
+    const int64_t units = int64_t(g.batch) * kv_heads;
+    int cluster = 1;
+    if (tiles > kCtaStepTiles)
+      while (cluster < 8 && units * 2 * cluster <= 2 * num_sms) cluster *= 2;
+    if (tiles <= int64_t(kClusterStepTiles) * cluster) {
       pl.parts = 0;
-      pl.ctas = g.batch * kv_heads;
+      pl.cluster = cluster;
+      pl.ctas = static_cast<int>(units * cluster);
       return pl;
     }
   }
@@ -217,6 +227,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   p.ws_ml = reinterpret_cast<float2*>(p.ws_o + size_t(2) * pl.ctas * pl.rows_cap * sea::pg::DH);
   p.rows_cap = pl.rows_cap;
   p.parts = pl.parts;
+  p.cluster = pl.cluster;
   p.least = 1;
   p.err = dev->err;
   p.limit_ns = sea::kDefaultTimeoutNs;
@@ -237,10 +248,18 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
                      sea::pg::ChunkCfg::SMEM_BYTES, stream, tq, tk, tv, cp);
     if (!cp.cut) return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   } else {
-    err = pl.rows_cap == 16 ? launch_pdl(sea::pg::paged_step_kernel<1>, dim3(pl.ctas), dim3(StepCfg<1>::THREADS),
-                                         StepCfg<1>::SMEM_BYTES, stream, tk, tv, p)
-                            : launch_pdl(sea::pg::paged_step_kernel<2>, dim3(pl.ctas), dim3(StepCfg<2>::THREADS),
-                                         StepCfg<2>::SMEM_BYTES, stream, tk, tv, p);
+    const unsigned cluster = static_cast<unsigned>(std::max(1, pl.cluster));
+    auto launch = [&](auto kernel, int threads, int smem) {
+      return launch_pdl_cluster(kernel, dim3(pl.ctas), dim3(threads), smem, stream, cluster, tk, tv, p);
+    };
+    using One = StepCfg<1>;
+    using Two = StepCfg<2>;
+    if (pl.rows_cap == 16)
+      err = pl.parts > 0 ? launch(sea::pg::paged_step_kernel<1, true>, One::THREADS, One::SMEM_BYTES)
+                         : launch(sea::pg::paged_step_kernel<1, false>, One::THREADS, One::SMEM_BYTES);
+    else
+      err = pl.parts > 0 ? launch(sea::pg::paged_step_kernel<2, true>, Two::THREADS, Two::SMEM_BYTES)
+                         : launch(sea::pg::paged_step_kernel<2, false>, Two::THREADS, Two::SMEM_BYTES);
   }
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
   if (pl.parts == 0) return ATTN_OK;

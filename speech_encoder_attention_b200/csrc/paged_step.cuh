@@ -15,10 +15,12 @@
 //   warps 0-3   warp w takes slots [32w, 32w + 32) of every key tile with a
 //               running max, sum and output of its own; warp 0 merges the
 //               four at the end of a unit.
-// The key tiles of all units are cut into equal parts, a CTA for each part and
-// K/V head, two CTAs per SM; units that are cut leave partials that
-// paged_combine_kernel merges. Where a unit has few key tiles at most, a CTA per
-// unit (and no second launch) takes less time than cutting and merging.
+// Two ways to deal out the work. Long caches: the key tiles of all units are cut
+// into equal parts, a CTA for each part and K/V head, two CTAs per SM; units that
+// are cut leave partials that paged_combine_kernel merges. Where a unit has few
+// key tiles: a cluster of up to 8 CTAs per unit, each with an equal run of its
+// tiles, merged through distributed shared memory, with no second launch and no
+// workspace.
 #pragma once
 
 #include "paged_common.cuh"
@@ -42,7 +44,8 @@ struct StepParams {
   float* ws_o;       // [2 * CTAs][rows_cap][64] unnormalised partial O
   float2* ws_ml;     // [2 * CTAs][rows_cap] (m in log2 units, l)
   int rows_cap;
-  int parts;         // the line of key tiles is cut into this many; 0: a CTA per unit
+  int parts;         // the line of key tiles is cut into this many; 0: a cluster per unit
+  int cluster;       // CTAs of that cluster, at most 8
   int least;         // fewest key tiles per part
   uint32_t* err;
   uint64_t limit_ns;
@@ -98,7 +101,7 @@ __device__ __forceinline__ void zero_rows(const StepParams& p, int b, int h, int
   }
 }
 
-template <int MT>
+template <int MT, bool CUT>
 __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
     paged_step_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const StepParams p) {
@@ -133,25 +136,32 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
   griddep_launch_dependents();
   const WaitCtl wc{abort_flag, p.err, p.limit_ns};
 
-  const int h = blockIdx.x % g.kv_heads;
+  const int h = (CUT ? blockIdx.x : blockIdx.x / p.cluster) % g.kv_heads;
+  // This CTA's partial for its cluster, in the place of warp 1's for warp 0.
+  float* part_of_cta = reinterpret_cast<float*>(smem + C::OFF_MERGE);
   Walk w;
   bool any;
-  if (p.parts > 0) {
+  if constexpr (CUT) {
     any = walk_start(g, w, blockIdx.x / g.kv_heads, p.parts, p.least);
   } else {
-    w.b = blockIdx.x / g.kv_heads;
+    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
+    w.b = unit / g.kv_heads;
     w.qt = 0;
     w.s = seq_of(g, w.b);
     w.u = span_of(g, w.s, 0);
-    w.k0 = 0;
-    w.k1 = w.u.n;
-    w.whole = true;
-    any = w.u.n > 0;
+    w.k0 = static_cast<int>(static_cast<long long>(w.u.n) * rank / p.cluster);
+    w.k1 = static_cast<int>(static_cast<long long>(w.u.n) * (rank + 1) / p.cluster);
+    w.whole = p.cluster == 1;
+    any = w.k1 > w.k0;
     // rows that see nothing: all of them, or the padding behind the valid ones
-    if (warp == 0) zero_rows(p, w.b, h, w.u.tok0 + (any ? w.u.ntok : 0), g.t_q);
+    if (warp == 0 && rank == 0) zero_rows(p, w.b, h, w.u.tok0 + (w.u.n > 0 ? w.u.ntok : 0), g.t_q);
+    if (warp == 0 && !any) {  // an empty partial
+#pragma unroll
+      for (int i = 0; i < MT * 4; ++i) part_of_cta[MT * 1024 + i * 32 + lane] = (i & 2) ? 0.f : -INFINITY;
+    }
   }
   // the next unit of this CTA
-  auto next_unit = [&]() { return p.parts > 0 && walk_next(g, w); };
+  auto next_unit = [&]() { return CUT && walk_next(g, w); };
   if (any && warp == C::WARPS) {
     // ---------------- producer ----------------
     const int n_pages = pages_per_tile(g);
@@ -409,6 +419,10 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
                 }
               }
             }
+            if (!CUT && !w.whole) {
+              part_of_cta[MT * 1024 + (m * 4 + e) * 32 + lane] = mx;
+              part_of_cta[MT * 1024 + (m * 4 + 2 + e) * 32 + lane] = l;
+            }
             const int r = 16 * m + 8 * e + r4;
             if (r < rows) {
               if (w.whole) {
@@ -423,7 +437,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
                       l != 0.f ? pack_half2(o[m][d][2 * e] * inv, o[m][d][2 * e + 1] * inv) : 0u;
                 if (p.lse != nullptr && c2 == 0)
                   p.lse[row * g.n_heads + head] = l != 0.f ? mx * kLn2 + logf(l) : -INFINITY;
-              } else {
+              } else if constexpr (CUT) {
                 const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + w.slot) * p.rows_cap + r;
                 float2* dst = reinterpret_cast<float2*>(p.ws_o + part * DH + c2);
 #pragma unroll
@@ -433,6 +447,12 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
             }
           }
         }
+        if (!CUT && !w.whole) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) part_of_cta[(m * 32 + i) * 32 + lane] = o[m][i >> 2][i & 3];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(merge_empty);
       }
@@ -440,6 +460,71 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
     } while (next_unit());
   }
   __syncthreads();
+  if (CUT || p.cluster == 1) return;
+  // The cluster's partials of the unit, merged as paged_combine_kernel does;
+  // rank r writes every cluster-th group of 8 columns, starting with its own.
+  cluster_sync();
+  if (warp == 0 && w.u.n > 0) {
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int r4 = lane >> 2, c2 = (lane & 3) * 2;
+    const uint32_t base = smem_u32(part_of_cta) + lane * 4;
+    auto load = [&](int i, int at) {
+      float v;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(base + at * 128, i)));
+      return v;
+    };
+    const int rows = w.u.ntok * g.group;
+#pragma unroll 1
+    for (int me = 0; me < 2 * MT && 8 * me < rows; ++me) {  // rows 8 me + lane / 4
+      const int m = me >> 1, e = me & 1;
+      const int r = 8 * me + r4;
+      // all of a row's loads before the first use: one round trip
+      float li[8], mi[8], x[8], y[8];
+      auto load_o = [&](int d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = i < p.cluster ? load(i, m * 32 + d * 4 + 2 * e) : 0.f;
+          y[i] = i < p.cluster ? load(i, m * 32 + d * 4 + 2 * e + 1) : 0.f;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        li[i] = i < p.cluster ? load(i, MT * 32 + m * 4 + 2 + e) : 0.f;
+        mi[i] = i < p.cluster ? load(i, MT * 32 + m * 4 + e) : 0.f;
+      }
+      load_o(rank);
+      float mx = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (li[i] != 0.f) mx = fmaxf(mx, mi[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mi[i] = li[i] != 0.f ? ex2_approx(mi[i] - mx) : 0.f;  // now the part's weight
+        if (li[i] != 0.f) l += li[i] * mi[i];
+      }
+      const int64_t row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + r / g.group;
+      const int head = h * g.group + r % g.group;
+      if (r < rows && p.sinks != nullptr && l != 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      for (int d = rank; d < 8; d += p.cluster) {
+        if (d != rank) load_o(d);
+        float a = 0.f, c = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (mi[i] != 0.f) {
+            a += x[i] * mi[i];
+            c += y[i] * mi[i];
+          }
+        }
+        if (r < rows)
+          *reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + head * DH + c2 + 8 * d) =
+              l != 0.f ? pack_half2(a * inv, c * inv) : 0u;
+      }
+      if (rank == 0 && c2 == 0 && r < rows && p.lse != nullptr)
+        p.lse[row * g.n_heads + head] = l != 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+    }
+  }
+  cluster_sync();  // no CTA leaves while another still reads its partial
 }
 
 // Merges the partials of cut units and writes the rows that no CTA holds.

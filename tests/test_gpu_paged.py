@@ -76,8 +76,8 @@ def inputs(name, slots=None):
     return c, rng, cache, batch, q, opts, q_lens, sinks
 
 
-# With few slots per sequence a CTA walks a whole unit; with many the units may be cut.
-@pytest.mark.parametrize("slots", [None, 5000])
+# Few slots per sequence: a CTA or a small cluster per unit; more: eight CTAs; many: units cut into parts.
+@pytest.mark.parametrize("slots", [None, 1500, 14000])
 @pytest.mark.parametrize("name", CASES)
 def test_attention_matches_the_oracle(name, slots):
     c, _, cache, batch, q, opts, q_lens, sinks = inputs(name, slots)
@@ -303,7 +303,7 @@ def test_a_decode_loop_with_eviction():
     assert evicted >= 1
 
 
-@pytest.mark.parametrize("slots", [400, 4000])
+@pytest.mark.parametrize("slots", [400, 16000])
 def test_captured_step_follows_its_inputs(slots):
     """One captured decode step replayed while lengths, pages and rows change."""
     rng = np.random.default_rng(12)
@@ -394,7 +394,7 @@ def test_another_device_and_stream_are_refused_or_followed():
         attn.attn_paged(q, cache, 1, 2, 2)
     with pytest.raises(ValueError):
         attn.attn_paged(q, cache, 2, 1, 2)
-    long = make_cache(rng, [90], 2, 16, slots=9000)
+    long = make_cache(rng, [90], 2, 16, slots=14000)
     assert attn.paged_workspace_size(cache, 1, 1, 2) == 0 < attn.paged_workspace_size(long, 1, 1, 2)
     with pytest.raises(attn.AttnError):
         attn.attn_paged(q, long, 1, 1, 2, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))

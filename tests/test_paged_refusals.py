@@ -155,3 +155,10 @@ def test_oracle_evict_keeps_order_ties_and_holes():
     assert oracle.evict_order([0], 8, w[0], 16, 1, 4, 2, 2) == [0, 1, 6, 7]
     assert oracle.evict_order([0], 3, w[0], 16, 1, 4, 0, 0) == [0, 1, 2]
     assert oracle.evict_order([-1, 0], 18, np.zeros(32), 16, 1, 4, 2, 1) == [16, 17]
+
+
+def test_packed_cache_structure_matches_the_c_layout():
+    c = attn.AttnPagedKV.from_buffer_copy(attn._PAGED_KV.pack(*range(1, 11)))
+    assert ctypes.sizeof(attn.AttnPagedKV) == attn._PAGED_KV.size
+    assert (c.k.ptr, c.k.row_stride, c.v.ptr, c.v.row_stride, c.table, c.kv_lens) == (1, 2, 3, 4, 5, 6)
+    assert (c.num_pages, c.page_size, c.pages_per_seq, c.n_kv_heads) == (7, 8, 9, 10)
