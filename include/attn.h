@@ -359,8 +359,8 @@ size_t attn_paged_weights_workspace_size(void);
  * slot, up to budget in all (NaN counts as -inf). What stays keeps its order:
  * kept slot n of sequence b moves to slot n of `dst` (rows of K and V), w_out[b, n]
  * takes its weight, kept[b, n] its old slot; w_out is 0 and kept is -1 behind the
- * last, and dst.kv_lens[b] is how many stayed. A row whose page in dst.table is
- * out of range is not moved.
+ * last, and dst.kv_lens[b] is how many stayed. dst.table must have pages for the
+ * slots that are filled: a row whose page is out of range is not moved, and lost.
  *   budget    >= 1, >= first + recent, at most dst's slots per sequence
  *   dst       page_size and n_kv_heads as the source. Either other pools
  *             (not overlapping the source's), or the same: then a page that is in

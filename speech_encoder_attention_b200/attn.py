@@ -392,6 +392,7 @@ class PagedKV(namedtuple("PagedKV", "k v table lens page_size n_kv_heads batch s
         return tuple.__new__(cls, (k, v, table, lens, page_size, n_kv_heads, batch, per_seq * page_size, dev, c))
 
 
+_INT_MAX = 2 ** 31 - 1
 _PAGED_KV = struct.Struct("@QqQqQQiiii")  # the fields of AttnPagedKV, in order
 
 
@@ -423,6 +424,12 @@ def _rows(t, what: str, rows: int, cols: int, device) -> AttnMat:
     if have != rows:
         raise ValueError(f"{what} must have {rows} rows, got {have}")
     return AttnMat(ptr, stride)
+
+
+def _paged_mask(window: int, first: int, causal, q_lens, batch: int, device) -> AttnPagedMask:
+    if not (0 <= window <= _INT_MAX and 0 <= first <= _INT_MAX):
+        raise ValueError(f"window and first must be 32-bit and not negative, got {window} and {first}")
+    return AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, device))
 
 
 def _batch_of(cache: PagedKV, batch: int) -> AttnPagedKV:
@@ -474,7 +481,7 @@ def attn_paged_append(k_new, v_new, cache: PagedKV, batch, t_new, q_lens=None, s
 
 def paged_workspace_size(cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal=True) -> int:
     """Bytes of workspace attn_paged needs for these sizes on the current device."""
-    mask = AttnPagedMask(window, first, 1 if causal else 0, 0)
+    mask = _paged_mask(window, first, causal, None, batch, cache.device)
     return int(load_library().attn_paged_workspace_size(_batch_of(cache, batch), batch, t_q, n_heads, mask))
 
 
@@ -509,7 +516,7 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
     lib = load_library()
     kv = _batch_of(cache, batch)
     qm = _rows(q, "q", rows, cols, dev)
-    mask = AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, dev))
+    mask = _paged_mask(window, first, causal, q_lens, batch, dev)
     sinks_ptr = 0 if sinks is None else _dev_tensor(sinks, "sinks", torch.float32, (n_heads,), dev)
     if out is None:
         out = q.new_empty((rows, cols))
@@ -551,7 +558,7 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
     lib = load_library()
     kv = _batch_of(cache, batch)
     qm = _rows(q, "q", rows, n_heads * HEAD_DIM, dev)
-    mask = AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, dev))
+    mask = _paged_mask(window, first, causal, q_lens, batch, dev)
     lse_ptr = _dev_tensor(lse, "lse", torch.float32, (rows, n_heads), dev)
     shape = (batch, cache.slots)
     w_in = 0 if weights is None else _dev_tensor(weights, "weights", torch.float32, shape, dev)
@@ -571,7 +578,8 @@ def attn_paged_evict(cache: PagedKV, weights, budget, first=0, recent=0, dst: Op
                      weights_out=None, stream=None):
     """Shrinks each sequence to its `first` first, `recent` last and heaviest
     slots, `budget` in all, in order, at the front of dst (None: in place, in
-    cache's own pages; cache.lens is updated). Returns (kept, weights):
+    cache's own pages; cache.lens is updated). dst's table must have a page for
+    each of the first `budget` slots: what would go to a hole is lost. Returns (kept, weights):
     kept [batch, budget] int32 holds the old slot of each new one (-1 behind the
     last), weights [batch, dst slots] the moved weights (0 behind the last).
     dst.lens is written. Without weights_out a new tensor is returned;

@@ -428,9 +428,9 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
       const int64_t out_row = static_cast<int64_t>(u.b) * g.t_q + u.tok0 + tok_r;
       const int head = u.h * g.group + head_r;
       __half* out = p.out + out_row * p.out_stride + head * DH;
-      float l_fin = row_ok ? l_run : 0.f;
-      if (whole && row_ok && p.sinks != nullptr && l_fin != 0.f) l_fin += ex2_approx(__ldg(p.sinks + head) * kLog2e - m_run);
-      const float inv = l_fin != 0.f ? 1.f / l_fin : 0.f;
+      const float l_fin = row_ok ? l_run : 0.f;
+      const RowEnd end = row_end(l_fin, m_run, whole && row_ok && p.sinks != nullptr ? __ldg(p.sinks + head) : -INFINITY);
+      const float inv = end.inv;
       const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + u.slot) * p.rows_cap + row;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
       }
       if (whole) {
         if (row_out && p.lse != nullptr)
-          p.lse[out_row * g.n_heads + head] = l_fin != 0.f ? m_run * kLn2 + logf(l_fin) : -INFINITY;
+          p.lse[out_row * g.n_heads + head] = end.lse;
       } else if (row_ok) {
         p.ws_ml[part] = make_float2(m_run, l_run);
       }

@@ -98,6 +98,26 @@ __device__ __forceinline__ Span span_of(const Geo& g, const Seq& s, int qt) {
   return u;
 }
 
+// The end of a row's softmax: what its unnormalised output is multiplied by, and
+// the log of its denominator, from the sum l with exponent reference m (log2
+// units) and the sink (-inf: none), whichever is larger being the common
+// reference. l = 0, a row that saw nothing, gives 0 and -inf.
+struct RowEnd {
+  float inv, lse;
+};
+
+__device__ __forceinline__ RowEnd row_end(float l, float m, float sink) {
+  if (l == 0.f) return RowEnd{0.f, -INFINITY};
+  const float s2 = sink * kLog2e;
+  if (s2 > m) {
+    const float down = ex2_approx(m - s2);
+    const float total = fmaf(l, down, 1.f);
+    return RowEnd{down / total, s2 * kLn2 + logf(total)};
+  }
+  const float total = l + ex2_approx(s2 - m);
+  return RowEnd{1.f / total, m * kLn2 + logf(total)};
+}
+
 // ---------------------------------------------------------------------------
 // work split: the key tiles of all (sequence, query tile) units in one line,
 // cut into equal parts; CTA part * kv_heads + h walks its part for K/V head h.

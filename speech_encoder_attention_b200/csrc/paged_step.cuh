@@ -428,15 +428,13 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
               if (w.whole) {
                 const int64_t row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + r / g.group;
                 const int head = h * g.group + r % g.group;
-                if (p.sinks != nullptr && l != 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
-                const float inv = l != 0.f ? 1.f / l : 0.f;
+                const RowEnd end = row_end(l, mx, p.sinks != nullptr ? __ldg(p.sinks + head) : -INFINITY);
                 __half* dst = p.out + row * p.out_stride + head * DH + c2;
 #pragma unroll
                 for (int d = 0; d < 8; ++d)
                   *reinterpret_cast<uint32_t*>(dst + 8 * d) =
-                      l != 0.f ? pack_half2(o[m][d][2 * e] * inv, o[m][d][2 * e + 1] * inv) : 0u;
-                if (p.lse != nullptr && c2 == 0)
-                  p.lse[row * g.n_heads + head] = l != 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+                      l != 0.f ? pack_half2(o[m][d][2 * e] * end.inv, o[m][d][2 * e + 1] * end.inv) : 0u;
+                if (p.lse != nullptr && c2 == 0) p.lse[row * g.n_heads + head] = end.lse;
               } else if constexpr (CUT) {
                 const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + w.slot) * p.rows_cap + r;
                 float2* dst = reinterpret_cast<float2*>(p.ws_o + part * DH + c2);
@@ -504,8 +502,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
       }
       const int64_t row = static_cast<int64_t>(w.b) * g.t_q + w.u.tok0 + r / g.group;
       const int head = h * g.group + r % g.group;
-      if (r < rows && p.sinks != nullptr && l != 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - mx);
-      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const RowEnd end = row_end(l, mx, p.sinks != nullptr && r < rows ? __ldg(p.sinks + head) : -INFINITY);
       for (int d = rank; d < 8; d += p.cluster) {
         if (d != rank) load_o(d);
         float a = 0.f, c = 0.f;
@@ -518,10 +515,9 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
         }
         if (r < rows)
           *reinterpret_cast<uint32_t*>(p.out + row * p.out_stride + head * DH + c2 + 8 * d) =
-              l != 0.f ? pack_half2(a * inv, c * inv) : 0u;
+              l != 0.f ? pack_half2(a * end.inv, c * end.inv) : 0u;
       }
-      if (rank == 0 && c2 == 0 && r < rows && p.lse != nullptr)
-        p.lse[row * g.n_heads + head] = l != 0.f ? mx * kLn2 + logf(l) : -INFINITY;
+      if (rank == 0 && c2 == 0 && r < rows && p.lse != nullptr) p.lse[row * g.n_heads + head] = end.lse;
     }
   }
   cluster_sync();  // no CTA leaves while another still reads its partial
@@ -645,12 +641,12 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const
   if (r >= rows_out || (r < rows && !cut)) return;  // rows of whole units are written already
   const int64_t row = static_cast<int64_t>(b) * g.t_q + u.tok0 + r / g.group;
   const int head = h * g.group + r % g.group;
-  if (p.sinks != nullptr && l != 0.f) l += ex2_approx(__ldg(p.sinks + head) * kLog2e - m);
-  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const RowEnd end = row_end(l, m, p.sinks != nullptr ? __ldg(p.sinks + head) : -INFINITY);
+  const float inv = end.inv;
   *reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * DH + c8) =
       make_uint4(pack_half2(o[0] * inv, o[1] * inv), pack_half2(o[2] * inv, o[3] * inv),
                  pack_half2(o[4] * inv, o[5] * inv), pack_half2(o[6] * inv, o[7] * inv));
-  if (p.lse != nullptr && c8 == 0) p.lse[row * g.n_heads + head] = l != 0.f ? m * kLn2 + logf(l) : -INFINITY;
+  if (p.lse != nullptr && c8 == 0) p.lse[row * g.n_heads + head] = end.lse;
 }
 
 }  // namespace pg

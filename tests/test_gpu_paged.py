@@ -81,11 +81,13 @@ def inputs(name, slots=None):
 @pytest.mark.parametrize("name", CASES)
 def test_attention_matches_the_oracle(name, slots):
     c, _, cache, batch, q, opts, q_lens, sinks = inputs(name, slots)
-    out = torch.full((batch * c["t_q"], c["heads"] * 64 + 8), 7.0, dtype=torch.float16, device="cuda")
-    got, lse = attn.attn_paged(q, cache, batch, c["t_q"], c["heads"], q_lens=i32(q_lens), sinks=sinks, out=out,
-                               return_lse=True, **opts)
-    assert (out[:, c["heads"] * 64:] == 7.0).all()
-    got = got[:, :c["heads"] * 64]
+    rows, cols = batch * c["t_q"], c["heads"] * 64
+    out = torch.full((rows + 3, cols + 8), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((rows + 3, c["heads"]), 7.0, device="cuda")
+    attn.attn_paged(q, cache, batch, c["t_q"], c["heads"], q_lens=i32(q_lens), sinks=sinks, out=out[:rows],
+                    lse=lse[:rows], **opts)
+    assert (out[:, cols:] == 7.0).all() and (out[rows:] == 7.0).all() and (lse[rows:] == 7.0).all()
+    got, lse = out[:rows, :cols], lse[:rows]
     k, v, table, lens = parts(cache)
     args = (table, lens, c["page"], c["t_q"], c["heads"], c["kv"])
     more = dict(q_lens=q_lens, sinks=None if sinks is None else sinks.cpu().numpy().astype(np.float64), **opts)
@@ -412,3 +414,29 @@ def test_nan_that_a_row_sees_comes_back_as_nan(t_q):
     assert torch.isnan(got[:t_q, :128]).all() and torch.isnan(lse[:t_q, :2]).all()
     assert torch.equal(got[:t_q, 128:], clean[:t_q, 128:]) and torch.equal(got[t_q:], clean[t_q:])
     assert torch.equal(lse[t_q:], clean_lse[t_q:])
+
+
+@pytest.mark.parametrize("slots", [None, 1500, 14000])
+@pytest.mark.parametrize("t_q", [1, 40])
+def test_sinks_far_above_and_below_the_scores(t_q, slots):
+    """A sink of 300 takes all the weight (output 0, lse the sink); one of -300 or -inf takes none."""
+    rng = np.random.default_rng(17)
+    cache = make_cache(rng, [200, 77], 4, 16, slots=slots)
+    q = queries(rng, 2, t_q, 4)
+    sinks = torch.tensor([300.0, -300.0, -float("inf"), 2.0], device="cuda")
+    got, lse = attn.attn_paged(q, cache, 2, t_q, 4, sinks=sinks, return_lse=True)
+    check_attention(got, lse, *attention64(q, cache, t_q, 4, sinks=sinks), 200)
+    assert (got[:, :64] == 0).all() and ((lse[:, 0] - 300.0).abs() <= 2.0 ** -14).all()  # 2 roundings of 300
+
+
+def test_numbers_that_do_not_fit_are_refused():
+    rng = np.random.default_rng(18)
+    cache = make_cache(rng, [20], 1, 16)
+    q = queries(rng, 1, 1, 1)
+    for bad in (dict(window=2 ** 32 + 1), dict(window=-1), dict(window=4, first=2 ** 31)):
+        with pytest.raises(ValueError):
+            attn.attn_paged(q, cache, 1, 1, 1, **bad)
+    with pytest.raises(attn.AttnError):
+        attn.attn_paged(q, cache, 1, 1, 1, first=3)
+    with pytest.raises(attn.AttnError):
+        attn.attn_paged_evict(cache, torch.zeros(1, 32, device="cuda"), 33)
