@@ -12,6 +12,10 @@
 //   move    bound by the bytes moved. Kept slot n comes from slot kept[n] >= n,
 //           so a CTA that owns some columns of a sequence and walks the rows
 //           upwards, loading a step before it stores it, may work in place.
+//
+// Measured on a B200, 20 K/V heads: appending 8 x 1500 rows 21.4 us = 5.7 TB/s;
+// evicting eight caches of 5 to 16 thousand slots down to 4096 into other pools
+// 69 us, 15 of them the selection, the move at 6.1 TB/s.
 #pragma once
 
 #include "flash_attn.cuh"
@@ -105,6 +109,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
   __shared__ uint32_t warp_sum[32], warp_eq[32];
   __shared__ uint32_t found[3];              // digit, how many of it are wanted, how many there are
   __shared__ uint32_t counts[2];             // this CTA's larger and equal keys
+  __shared__ uint32_t bases[4];              // both in the CTAs before this one, and in all
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int rank = blockIdx.x, ranks = gridDim.x, b = blockIdx.y;
   if (t < 512) hist[t >> 8][t & 255] = 0u;
@@ -123,6 +128,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
   // first `want` equal ones.
   uint32_t prefix = 0, limit = 1, want = static_cast<uint32_t>(p.budget);
   bool equal = false;  // `limit` is one key's value and only `want` of it stay
+  uint32_t n_gt = 0, n_eq = 0;  // this CTA's larger and equal keys, summed over threads
   for (int pass = 0; pass < 4; ++pass) {
     const int shift = 24 - 8 * pass;
     uint32_t* h = hist[pass & 1];
@@ -135,8 +141,9 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
       if (in && lane == __ffs(same) - 1) atomicAdd(&h[digit], __popc(same));
     }
     cluster_sync();
-    uint32_t mine = 0, above = 0;
+    uint32_t mine = 0, own = 0, above = 0;
     if (t < 256) {
+      own = h[255 - t];
       for (int r = 0; r < ranks; ++r) mine += ld_shared_cluster_u32(&h[255 - t], r);  // thread t: digit 255 - t
       uint32_t incl = mine;
 #pragma unroll
@@ -159,7 +166,17 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
       hist[(pass + 1) & 1][t] = 0u;  // read by others before the last barrier
     }
     __syncthreads();
-    if (found[2] == 0u) break;  // fewer slots than the budget: all stay
+    const bool some = found[2] != 0u;  // else fewer slots than the budget: all stay
+    if (t < 256) {
+      const uint32_t digit = 255 - t;
+      if (!some || digit > found[0])
+        n_gt += own;
+      else if (digit == found[0] && found[2] == found[1])
+        n_gt += own;  // every key of this digit stays
+      else if (digit == found[0] && pass == 3)
+        n_eq += own;
+    }
+    if (!some) break;
     prefix = prefix << 8 | found[0];
     want = found[1];
     limit = prefix << shift;
@@ -169,12 +186,6 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
   auto larger = [&](uint32_t key) { return key != 0u && (equal ? key > limit : key >= limit); };
 
   // Number what stays, in order. Earlier CTAs' counts first.
-  uint32_t n_gt = 0, n_eq = 0;
-  for (int j = ja + t; j < jz; j += SELECT_THREADS) {
-    const uint32_t key = key_at(j);
-    n_gt += larger(key);
-    n_eq += equal && key == limit;
-  }
   n_gt = __reduce_add_sync(0xffffffffu, n_gt);
   n_eq = __reduce_add_sync(0xffffffffu, n_eq);
   if (lane == 0) {
@@ -187,18 +198,20 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
     counts[1] = __reduce_add_sync(0xffffffffu, warp_eq[lane]);
   }
   cluster_sync();
-  uint32_t base_gt = 0, base_eq = 0, total = 0, total_eq = 0;
-  for (int r = 0; r < ranks; ++r) {
-    const uint32_t x = ld_shared_cluster_u32(&counts[0], r), y = ld_shared_cluster_u32(&counts[1], r);
-    if (r < rank) {
-      base_gt += x;
-      base_eq += y;
-    }
-    total += x;
-    total_eq += y;
+  if (warp == 0) {  // lane r: CTA r's counts
+    const uint32_t x = lane < ranks ? ld_shared_cluster_u32(&counts[0], lane) : 0u;
+    const uint32_t y = lane < ranks ? ld_shared_cluster_u32(&counts[1], lane) : 0u;
+    bases[0] = __reduce_add_sync(0xffffffffu, lane < rank ? x : 0u);
+    bases[1] = __reduce_add_sync(0xffffffffu, lane < rank ? y : 0u);
+    bases[2] = __reduce_add_sync(0xffffffffu, x);
+    bases[3] = __reduce_add_sync(0xffffffffu, y);
   }
+  __syncthreads();
+  uint32_t base_gt = bases[0], base_eq = bases[1];
+  const uint32_t total = bases[2], total_eq = bases[3];
   const int count = static_cast<int>(total + min(total_eq, equal ? want : 0u));
   int* kept = p.kept + static_cast<int64_t>(b) * p.budget;
+  const bool w_apart = p.w_out != nullptr && p.w_out != p.w_in;
   for (int j0 = ja; j0 < jz; j0 += SELECT_THREADS) {
     const int j = j0 + t;
     const uint32_t key = j < jz ? key_at(j) : 0u;
@@ -213,27 +226,34 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
     const uint32_t xg = warp_sum[lane], xe = warp_eq[lane], below = (1u << lane) - 1u;
     const uint32_t g_before = base_gt + __reduce_add_sync(0xffffffffu, lane < warp ? xg : 0u) + __popc(bg & below);
     const uint32_t e_before = base_eq + __reduce_add_sync(0xffffffffu, lane < warp ? xe : 0u) + __popc(be & below);
-    if (gt || (eq && e_before < want)) kept[g_before + min(e_before, want)] = j;
+    if (gt || (eq && e_before < want)) {
+      const uint32_t n = g_before + min(e_before, want);
+      kept[n] = j;
+      if (w_apart) p.w_out[static_cast<int64_t>(b) * p.out_cap + n] = w[j];
+    }
     base_gt += __reduce_add_sync(0xffffffffu, xg);
     base_eq += __reduce_add_sync(0xffffffffu, xe);
   }
   for (int n = count + rank * SELECT_THREADS + t; n < p.budget; n += ranks * SELECT_THREADS) kept[n] = -1;
 
-  // The weights move like the rows: n <= kept[n], so with a barrier between the
-  // reads and the writes of a step w_out may be w_in.
-  __threadfence();  // kept, for the other CTAs
-  cluster_sync();
+  // Weights in place move like the rows: n <= kept[n], so a barrier between the
+  // reads and the writes of a step is enough.
   if (p.w_out != nullptr) {
     float* w_out = p.w_out + static_cast<int64_t>(b) * p.out_cap;
-    for (int n0 = 0; n0 < count; n0 += ranks * SELECT_THREADS) {
-      const int n = n0 + rank * SELECT_THREADS + t;
-      float x = 0.f;
-      if (n < count) x = w[*const_cast<const volatile int*>(kept + n)];
+    if (!w_apart) {
+      __threadfence();  // kept, for the other CTAs
       cluster_sync();
-      if (n < count) w_out[n] = x;
+      for (int n0 = 0; n0 < count; n0 += ranks * SELECT_THREADS) {
+        const int n = n0 + rank * SELECT_THREADS + t;
+        float x = 0.f;
+        if (n < count) x = w[*const_cast<const volatile int*>(kept + n)];
+        cluster_sync();
+        if (n < count) w_out[n] = x;
+      }
     }
     for (int n = count + rank * SELECT_THREADS + t; n < p.out_cap; n += ranks * SELECT_THREADS) w_out[n] = 0.f;
   }
+  cluster_sync();  // every CTA has read the lengths, and the counts of this one
   if (rank == 0 && t == 0) p.out_lens[b] = count;
 }
 

@@ -15,6 +15,16 @@
 // most, first, every other round in reverse order of the CTAs so that the shares
 // come out even. With few, the key tiles of all units are cut into equal parts as
 // in paged_step_kernel, and paged_combine_kernel merges what was cut.
+//
+// Measured on a B200, 20 heads: eight causal prompts of 1500 tokens 113 us = 408
+// TFLOP/s over the visible pairs (46 % of the exponential rate, 21 % of the
+// tensor pipe); four ragged chunks of up to 509 tokens over up to 6007 slots, 4
+// K/V heads, 83 us = 433 TFLOP/s. A key tile takes a softmax thread about 3100
+// cycles, 1024 of them exponentials, and the two CTAs of an SM overlap only in
+// part; leaving out the page and window checks would give 8 %. Slower, each
+// tried: two threads per row with 64 columns each (130 and 104 us), exponentials
+// on half a tile while the other half's max is taken (120 and 87 us), part of
+// the exponentials as polynomials (123 and 88 us at an eighth).
 #pragma once
 
 #include "flash_attn.cuh"

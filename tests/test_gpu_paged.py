@@ -213,6 +213,7 @@ EVICT = [
     dict(lens=[50], budget=1, first=0, recent=0, page=16),
     dict(lens=[20, 90], budget=64, first=2, recent=3, page=16, holes=[(0, 1), (1, 0), (1, 3)]),
     dict(lens=[33], budget=12, first=2, recent=2, page=16, holes=[(0, 0), (0, 1), (0, 2)]),
+    dict(lens=[70001], budget=3001, first=7, recent=500, page=256),  # more keys than shared memory holds
 ]
 
 
