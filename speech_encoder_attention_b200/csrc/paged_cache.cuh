@@ -14,8 +14,8 @@
 //           upwards, loading a step before it stores it, may work in place.
 //
 // Measured on a B200, 20 K/V heads: appending 8 x 1500 rows 21.4 us = 5.7 TB/s;
-// evicting eight caches of 5 to 16 thousand slots down to 4096 into other pools
-// 69 us, 15 of them the selection, the move at 6.1 TB/s.
+// evicting eight caches of 7 to 16 thousand slots down to 4096 into other pools
+// 69 us, 15 of them the selection, the move at 6.1 TB/s; in place 96 us.
 #pragma once
 
 #include "flash_attn.cuh"
@@ -258,10 +258,11 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
 }
 
 // Moves the rows of the kept slots: CTA (row range, columns of K or of V,
-// sequence), a step of MOVE_STEPS 16-byte pieces per thread, row by row.
+// sequence), MOVE_STEPS 16-byte pieces per thread and step, row by row.
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_STEPS = 4;
 
+template <bool SAME_POOL>
 __global__ void __launch_bounds__(MOVE_THREADS) paged_move_kernel(const EvictParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -279,28 +280,80 @@ __global__ void __launch_bounds__(MOVE_THREADS) paged_move_kernel(const EvictPar
   const int* t_in = p.g.table + static_cast<int64_t>(b) * p.g.pages_per_seq;
   const int* t_out = p.out_table + static_cast<int64_t>(b) * p.out_pages_per_seq;
   const int pieces = (n_end - n_begin) * p.move_vecs;  // below 2^23 * 8, or a few rows
-  for (int x0 = 0; x0 < pieces; x0 += MOVE_THREADS * MOVE_STEPS) {
+  constexpr int STEP = MOVE_THREADS * MOVE_STEPS;
+  if constexpr (!SAME_POOL) {
+    for (int x0 = 0; x0 < pieces; x0 += STEP) {
+      uint4 x[MOVE_STEPS];
+      int64_t to[MOVE_STEPS];
+#pragma unroll
+      for (int i = 0; i < MOVE_STEPS; ++i) {
+        const int at = x0 + i * MOVE_THREADS + static_cast<int>(threadIdx.x);
+        to[i] = -1;
+        if (at >= pieces) continue;
+        const int row = fa::div_c(at, p.dv_vecs);
+        const int vec = at - row * p.move_vecs;
+        const int n = n_begin + row;
+        const int j = kept[n];
+        if (j < 0) continue;
+        const int pi = t_in[j >> p.g.page_shift], po = t_out[n >> p.g.page_shift];
+        if (po < 0 || po >= p.out_num_pages) continue;
+        to[i] = ((static_cast<int64_t>(po) << p.g.page_shift) + (n & mask)) * ds + vec;
+        x[i] = src[((static_cast<int64_t>(pi) << p.g.page_shift) + (j & mask)) * ss + vec];
+      }
+#pragma unroll
+      for (int i = 0; i < MOVE_STEPS; ++i)
+        if (to[i] >= 0) dst[to[i]] = x[i];
+    }
+    return;
+  }
+  struct Step {
     uint4 x[MOVE_STEPS];
     int64_t to[MOVE_STEPS];
+  };
+  auto slots = [&](int x0, int (&j)[MOVE_STEPS]) {
 #pragma unroll
     for (int i = 0; i < MOVE_STEPS; ++i) {
       const int at = x0 + i * MOVE_THREADS + static_cast<int>(threadIdx.x);
-      to[i] = -1;
-      if (at >= pieces) continue;
+      j[i] = at < pieces ? kept[n_begin + fa::div_c(at, p.dv_vecs)] : -1;
+    }
+  };
+  auto load = [&](int x0, const int (&j)[MOVE_STEPS], Step& s) {
+#pragma unroll
+    for (int i = 0; i < MOVE_STEPS; ++i) {
+      const int at = x0 + i * MOVE_THREADS + static_cast<int>(threadIdx.x);
+      s.to[i] = -1;
+      if (j[i] < 0) continue;
       const int row = fa::div_c(at, p.dv_vecs);
       const int vec = at - row * p.move_vecs;
       const int n = n_begin + row;
-      const int j = kept[n];
-      if (j < 0) continue;
-      const int pi = t_in[j >> p.g.page_shift], po = t_out[n >> p.g.page_shift];
+      const int pi = t_in[j[i] >> p.g.page_shift], po = t_out[n >> p.g.page_shift];
       if (po < 0 || po >= p.out_num_pages) continue;
-      to[i] = ((static_cast<int64_t>(po) << p.g.page_shift) + (n & mask)) * ds + vec;
-      x[i] = src[((static_cast<int64_t>(pi) << p.g.page_shift) + (j & mask)) * ss + vec];
+      s.to[i] = ((static_cast<int64_t>(po) << p.g.page_shift) + (n & mask)) * ds + vec;
+      s.x[i] = src[((static_cast<int64_t>(pi) << p.g.page_shift) + (j[i] & mask)) * ss + vec];
     }
+  };
+  auto store = [&](const Step& s) {
     __syncthreads();  // this step's rows are read before any is overwritten
 #pragma unroll
     for (int i = 0; i < MOVE_STEPS; ++i)
-      if (to[i] >= 0) dst[to[i]] = x[i];
+      if (s.to[i] >= 0) dst[s.to[i]] = s.x[i];
+  };
+  // Two steps are on their way at a time, and the slots of the third are known:
+  // what a step loads lies at or behind its own destinations, so the step before
+  // cannot overwrite it. Eight 16000-slot caches to 4096 in place: 96 us against
+  // 135 us one step at a time.
+  int j[MOVE_STEPS];
+  Step a, c;
+  slots(0, j);
+  load(0, j, a);
+  slots(STEP, j);
+  for (int x0 = 0; x0 < pieces; x0 += 2 * STEP) {
+    load(x0 + STEP, j, c);
+    slots(x0 + 2 * STEP, j);
+    store(a);
+    load(x0 + 2 * STEP, j, a);
+    slots(x0 + 3 * STEP, j);
+    store(c);
   }
 }
 

@@ -396,7 +396,8 @@ attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budge
   p.move_vecs = same ? sea::pg::DH / 8 : row_vecs;
   p.dv_vecs = make_divc(p.move_vecs);
   const dim3 grid(ceil_div(budget, p.rows_per_cta), 2 * (row_vecs / p.move_vecs), batch);
-  if (launch_pdl(sea::pg::paged_move_kernel, grid, dim3(sea::pg::MOVE_THREADS), 0, stream, p) != cudaSuccess)
+  if (launch_pdl(same ? sea::pg::paged_move_kernel<true> : sea::pg::paged_move_kernel<false>, grid,
+                 dim3(sea::pg::MOVE_THREADS), 0, stream, p) != cudaSuccess)
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }

@@ -22,7 +22,7 @@
 // tiles, merged through distributed shared memory, with no second launch and no
 // workspace.
 //
-// Measured on a B200, 20 heads, one token each: 16 sequences of 2.8 to 8.2
+// Measured on a B200, 20 heads, one token each: 16 sequences of 3.1 to 8.2
 // thousand slots 80 us = 5.9 TB/s of K and V, 0.90 of the copy rate (its TMA
 // loads alone take 78 us); 48 sequences with a 1024-slot window and 5 K/V heads
 // 17 us = 3.7 TB/s; one sequence 6.5 us at 448 slots, 8.2 us at 3000.
