@@ -341,16 +341,17 @@ size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q
  *   lse    [batch*t_q, n_heads] fp32
  *   w_in   [batch, pages_per_seq*page_size] fp32, or NULL for zeros
  *   w_out  the same shape; w_in itself, or not overlapping it
- * workspace: at least attn_paged_weights_workspace_size() bytes, 16-byte
- * aligned; NULL or a smaller one returns ATTN_ERR_INVALID. Calls that may run at
- * the same time need a workspace each.
+ * workspace: at least attn_paged_weights_workspace_size(...) bytes, 16-byte
+ * aligned (NULL with 0 bytes where that is 0); a smaller one returns
+ * ATTN_ERR_INVALID. Calls that may run at the same time need a workspace each.
  */
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                attn_paged_mask mask, const float *lse, float scale, const float *w_in, float *w_out,
                                void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
-/* Bytes of workspace attn_paged_weights needs on the current device, whatever the sizes (0 without a device). */
-size_t attn_paged_weights_workspace_size(void);
+/* Bytes of workspace attn_paged_weights needs for these sizes on the current device (0 for none, and for
+   invalid sizes). */
+size_t attn_paged_weights_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads);
 
 /*
  * attn_paged_evict -- shrinks each sequence to at most `budget` slots
@@ -361,6 +362,8 @@ size_t attn_paged_weights_workspace_size(void);
  * takes its weight, kept[b, n] its old slot; w_out is 0 and kept is -1 behind the
  * last, and dst.kv_lens[b] is how many stayed. dst.table must have pages for the
  * slots that are filled: a row whose page is out of range is not moved, and lost.
+ * Positions are slots: afterwards the rows keep their order, new tokens follow
+ * the last kept slot, and a window counts kept slots.
  *   budget    >= 1, >= first + recent, at most dst's slots per sequence
  *   dst       page_size and n_kv_heads as the source. Either other pools
  *             (not overlapping the source's), or the same: then a page that is in

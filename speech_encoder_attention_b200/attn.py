@@ -131,7 +131,8 @@ SIGNATURES = {
                                   ctypes.c_size_t, ctypes.c_void_p]),
     "attn_paged_workspace_size": (ctypes.c_size_t, [AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                                     AttnPagedMask]),
-    "attn_paged_weights_workspace_size": (ctypes.c_size_t, []),
+    "attn_paged_weights_workspace_size": (ctypes.c_size_t, [AttnPagedKV, ctypes.c_int32, ctypes.c_int32,
+                                                            ctypes.c_int32]),
     "attn_paged_weights": (ctypes.c_int, [AttnMat, AttnPagedKV, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                           AttnPagedMask, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
@@ -485,9 +486,9 @@ def paged_workspace_size(cache: PagedKV, batch, t_q, n_heads, window=0, first=0,
     return int(load_library().attn_paged_workspace_size(_batch_of(cache, batch), batch, t_q, n_heads, mask))
 
 
-def paged_weights_workspace_size() -> int:
-    """Bytes of workspace attn_paged_weights needs on the current device."""
-    return int(load_library().attn_paged_weights_workspace_size())
+def paged_weights_workspace_size(cache: PagedKV, batch, t_q, n_heads) -> int:
+    """Bytes of workspace attn_paged_weights needs for these sizes on the current device."""
+    return int(load_library().attn_paged_weights_workspace_size(_batch_of(cache, batch), batch, t_q, n_heads))
 
 
 def _given_workspace(workspace, device):
@@ -519,7 +520,7 @@ def attn_paged(q, cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal
     mask = _paged_mask(window, first, causal, q_lens, batch, dev)
     sinks_ptr = 0 if sinks is None else _dev_tensor(sinks, "sinks", torch.float32, (n_heads,), dev)
     if out is None:
-        out = q.new_empty((rows, cols))
+        out = torch.empty_like(q) if q.shape[1] == cols and q.is_contiguous() else q.new_empty((rows, cols))
         om = AttnMat(out.data_ptr(), cols)
     else:
         om = _rows(out, "out", rows, cols, dev)
@@ -548,7 +549,7 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
     """What attn_paged's rows put on each slot, summed over rows and heads, added
     to weights ([batch, cache.slots] fp32; None: zeros). lse is attn_paged's.
     Returns out, a new tensor unless given; out=weights adds in place. Without
-    workspace one is allocated for the call."""
+    workspace one is allocated for the call, if it needs any."""
     import torch
     dev, rows = cache.device, batch * t_q
     if _elsewhere(torch, dev, stream):
@@ -565,9 +566,13 @@ def attn_paged_weights(q, cache: PagedKV, lse, batch, t_q, n_heads, window=0, fi
     if out is None:
         out = lse.new_empty(shape)
     w_out = _dev_tensor(out, "out", torch.float32, shape, dev)
-    if workspace is None:
-        workspace = lse.new_empty(lib.attn_paged_weights_workspace_size(), dtype=torch.uint8)
-    ws_ptr, ws_bytes = _given_workspace(workspace, dev)
+    if workspace is not None:
+        ws_ptr, ws_bytes = _given_workspace(workspace, dev)
+    else:
+        ws_ptr, ws_bytes = 0, lib.attn_paged_weights_workspace_size(kv, batch, t_q, n_heads)
+        if ws_bytes:
+            workspace = lse.new_empty(ws_bytes, dtype=torch.uint8)
+            ws_ptr = workspace.data_ptr()
     st = lib.attn_paged_weights(qm, kv, batch, t_q, n_heads, mask, lse_ptr, scale, w_in, w_out, ws_ptr, ws_bytes,
                                 torch._C._cuda_getCurrentRawStream(dev.index))
     _check(st, "attn_paged_weights")

@@ -710,10 +710,11 @@ size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q
   return plan_paged(paged_geo(cache, batch, t_q, n_heads, mask), dev->num_sms).ws_bytes;
 }
 
-size_t attn_paged_weights_workspace_size(void) {
+size_t attn_paged_weights_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads) {
+  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch)) return 0;
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != ATTN_OK) return 0;
-  return paged_weights_workspace(sea::pg::WeightCfg<16>::CTAS_PER_SM * dev->num_sms);
+  return plan_weights(paged_geo(cache, batch, t_q, n_heads, attn_paged_mask{}), dev->num_sms).ws_bytes;
 }
 
 attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,

@@ -102,8 +102,10 @@ bool encode_paged_q(CUtensorMap* m, const attn_mat& q, int batch, int t_q, int n
          CUDA_SUCCESS;
 }
 
-// Chunks with at least this many units per CTA are walked unit by unit.
+// Chunks with at least this many units per CTA, or with at most this many key
+// tiles per unit, are walked unit by unit.
 constexpr int kWholeUnitsPerCta = 4;
+constexpr int kWholeChunkTiles = 8;
 
 // A unit of paged_step_kernel gets a cluster of its own instead of being cut into
 // parts where a CTA of it has at most kClusterStepTiles key tiles, and a single CTA
@@ -116,8 +118,8 @@ constexpr int kClusterStepTiles = 12;
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
   int tok_per_tile, q_tiles;
-  int parts, ctas;    // CTAs: one per part and K/V head, or (parts 0)
-  int cluster;        // so many per unit
+  int parts, ctas;    // CTAs: one per part and K/V head; parts 0: nothing is cut, and
+  int cluster;        // a step has so many per unit, a chunk walks whole units
   size_t ws_bytes;
 };
 
@@ -131,15 +133,15 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
   pl.q_tiles = ceil_div(t_q, pl.tok_per_tile);
   pl.parts = std::max(1, 2 * num_sms / kv_heads);
   pl.ctas = pl.parts * kv_heads;
+  const int64_t units = int64_t(g.batch) * kv_heads * pl.q_tiles;
+  // The cache bounds a unit's key tiles, or the window (its other side too
+  // unless causal), whose ends fall inside tiles, and the first tokens.
+  int64_t tiles = ceil_div(g.cap, sea::pg::BKV);
+  if (g.window > 0) {
+    const int64_t reach = int64_t(g.causal ? 1 : 2) * g.window + pl.tok_per_tile;
+    tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
+  }
   if (pl.rows_cap <= 32) {
-    // The cache bounds a unit's key tiles, or the window (its other side too
-    // unless causal), whose ends fall inside tiles, and the first tokens.
-    int64_t tiles = ceil_div(g.cap, sea::pg::BKV);
-    if (g.window > 0) {
-      const int64_t reach = int64_t(g.causal ? 1 : 2) * g.window + t_q;
-      tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
-    }
-    const int64_t units = int64_t(g.batch) * kv_heads;
     int cluster = 1;
     if (tiles > kCtaStepTiles)
       while (cluster < 8 && units * 2 * cluster <= 2 * num_sms) cluster *= 2;
@@ -149,6 +151,10 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
       pl.ctas = static_cast<int>(units * cluster);
       return pl;
     }
+  } else if (tiles <= kWholeChunkTiles || units >= int64_t(kWholeUnitsPerCta) * 2 * num_sms) {
+    pl.parts = 0;
+    pl.ctas = static_cast<int>(std::min<int64_t>(units, int64_t(2) * num_sms));
+    return pl;
   }
   pl.ws_bytes = size_t(2) * pl.ctas * pl.rows_cap * (sea::pg::DH * sizeof(float) + sizeof(float2));
   return pl;
@@ -239,14 +245,12 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
     sea::pg::ChunkParams cp{};
     cp.s = p;
     cp.units = static_cast<int>(units);
-    cp.cut = units < int64_t(kWholeUnitsPerCta) * 2 * dev->num_sms ? 1 : 0;
+    cp.cut = pl.parts > 0 ? 1 : 0;
     cp.dv_group = make_divc(p.g.group);
     cp.dv_heads = make_divc(cache.n_kv_heads);
     cp.dv_bh = make_divc(batch * cache.n_kv_heads);
-    const int grid = cp.cut ? pl.ctas : static_cast<int>(std::min<int64_t>(units, int64_t(2) * dev->num_sms));
-    err = launch_pdl(sea::pg::paged_chunk_kernel, dim3(grid), dim3(sea::pg::ChunkCfg::THREADS),
+    err = launch_pdl(sea::pg::paged_chunk_kernel, dim3(pl.ctas), dim3(sea::pg::ChunkCfg::THREADS),
                      sea::pg::ChunkCfg::SMEM_BYTES, stream, tq, tk, tv, cp);
-    if (!cp.cut) return err == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   } else {
     const unsigned cluster = static_cast<unsigned>(std::max(1, pl.cluster));
     auto launch = [&](auto kernel, int threads, int smem) {
@@ -272,8 +276,44 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   return ATTN_OK;
 }
 
-// Sums and states of the CTAs of paged_weights_kernel, at most four per SM.
-size_t paged_weights_workspace(int ctas) { return size_t(ctas) * (2 * sea::pg::BKV + 3) * 4; }
+// A cluster per key tile of paged_weights_kernel where no CTA of it gets more items
+// than this (0.6 us each, 1.2 us of 128 rows) and all clusters fit the device at
+// once. One token over up to 6000 slots, us: 4 K/V heads 6.4, cut and merged 7.3 to
+// 7.9; 20 heads 7.6 in clusters of 4, 8.5 to 9.5 cut, 16 in one CTA; 100 tokens of
+// 4 K/V heads 16 in clusters of 2, 10 cut.
+constexpr int kClusterTileItems = 5;
+constexpr int kClusterTileWideItems = 3;
+
+struct WeightPlan {
+  int rows;            // rows of a query tile: as few as hold the chunk, in whole tokens
+  int tok_per_tile, q_tiles;
+  int tiles;           // key tiles per sequence
+  int cluster;         // CTAs per key tile; 0: shares of the line of items
+  int ctas;
+  size_t ws_bytes;     // sums and states of the CTAs
+};
+
+WeightPlan plan_weights(const sea::pg::Geo& g, int num_sms) {
+  WeightPlan pl{};
+  const int64_t rows = static_cast<int64_t>(g.t_q) * g.group;
+  pl.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+  pl.tok_per_tile = std::min(g.t_q, pl.rows / g.group);
+  pl.q_tiles = ceil_div(g.t_q, pl.tok_per_tile);
+  pl.tiles = ceil_div(g.cap, sea::pg::BKV);
+  pl.ctas = (pl.rows == 128 ? sea::pg::WeightCfg<128>::CTAS_PER_SM : sea::pg::WeightCfg<16>::CTAS_PER_SM) * num_sms;
+  const int64_t key_tiles = static_cast<int64_t>(g.batch) * pl.tiles;
+  const int64_t items = static_cast<int64_t>(g.kv_heads) * pl.q_tiles;
+  pl.cluster = 1;
+  const int64_t most = pl.rows == 128 ? kClusterTileWideItems : kClusterTileItems;
+  while (pl.cluster < 8 && items > most * pl.cluster) pl.cluster *= 2;
+  if (items <= most * pl.cluster && key_tiles * pl.cluster <= pl.ctas) {
+    pl.ctas = static_cast<int>(key_tiles * pl.cluster);
+  } else {
+    pl.cluster = 0;
+    pl.ws_bytes = size_t(pl.ctas) * (2 * sea::pg::BKV + 3) * 4;
+  }
+  return pl;
+}
 
 attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
                                  attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
@@ -292,18 +332,21 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   if (overlaps(rw, mat_range(q.ptr, rows, cols, q.row_stride)) || overlaps(rw, byte_range(lse, 4 * rows * n_heads)) ||
       overlaps(rw, pool_range(cache, cache.k)))
     return ATTN_ERR_INVALID;
-  if (workspace == nullptr || !aligned16(workspace)) return ATTN_ERR_INVALID;
+  if (!aligned16(workspace) || (workspace == nullptr && workspace_bytes != 0)) return ATTN_ERR_INVALID;
 
   DeviceInfo* dev = nullptr;
   if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
   sea::pg::WeightParams p{};
   p.g = paged_geo(cache, batch, t_q, n_heads, mask);
-  const int64_t group_rows = static_cast<int64_t>(t_q) * p.g.group;
-  // Rows of a query tile: as few as hold the chunk, a whole number of tokens.
-  const int n = group_rows <= 16 ? 16 : group_rows <= 32 ? 32 : 128;
-  p.g.tok_per_tile = static_cast<int>(std::min<int64_t>(t_q, n / p.g.group));
-  p.g.q_tiles = ceil_div(t_q, p.g.tok_per_tile);
+  const WeightPlan pl = plan_weights(p.g, dev->num_sms);
+  if (workspace_bytes < pl.ws_bytes) return ATTN_ERR_INVALID;
+  p.g.tok_per_tile = pl.tok_per_tile;
+  p.g.q_tiles = pl.q_tiles;
   p.dv_group = make_divc(p.g.group);
+  p.tiles = pl.tiles;
+  p.cluster = pl.cluster;
+  p.ws_sum = static_cast<float*>(workspace);
+  p.ws_state = reinterpret_cast<int*>(p.ws_sum + size_t(pl.ctas) * 2 * sea::pg::BKV);
   p.lse = lse;
   p.w_in = w_in;
   p.w_out = w_out;
@@ -313,25 +356,23 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   CUtensorMap tq, tk;
   if (!encode_paged_q(&tq, q, batch, t_q, n_heads, p.g.group, p.g.tok_per_tile) || !encode_pages(&tk, cache, cache.k))
     return ATTN_ERR_CUDA;
-  p.tiles = ceil_div(p.g.cap, sea::pg::BKV);
   if (static_cast<int64_t>(batch) * p.tiles > INT32_MAX ||
-      static_cast<int64_t>(cache.n_kv_heads) * ceil_div(t_q, p.g.tok_per_tile) > INT32_MAX)
+      static_cast<int64_t>(cache.n_kv_heads) * pl.q_tiles > INT32_MAX)
     return ATTN_ERR_INVALID;
-  auto launch = [&](auto kernel, auto cfg) -> attn_status {
+  auto launch = [&](auto kernel, auto cfg) {
     using C = decltype(cfg);
-    const int ctas = C::CTAS_PER_SM * dev->num_sms;
-    if (workspace_bytes < paged_weights_workspace(ctas)) return ATTN_ERR_INVALID;
-    p.ws_sum = static_cast<float*>(workspace);
-    p.ws_state = reinterpret_cast<int*>(p.ws_sum + size_t(ctas) * 2 * sea::pg::BKV);
-    if (launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::SMEM_BYTES, stream, tq, tk, p) != cudaSuccess ||
-        launch_pdl(sea::pg::paged_weights_merge_kernel, dim3(ctas), dim3(sea::pg::BKV), 0, stream, p) != cudaSuccess)
-      return ATTN_ERR_CUDA;
-    return ATTN_OK;
+    return launch_pdl_cluster(kernel, dim3(pl.ctas), dim3(C::THREADS), C::SMEM_BYTES, stream,
+                              static_cast<unsigned>(std::max(1, pl.cluster)), tq, tk, p);
   };
   using sea::pg::WeightCfg;
-  return n == 16   ? launch(sea::pg::paged_weights_kernel<16>, WeightCfg<16>{})
-         : n == 32 ? launch(sea::pg::paged_weights_kernel<32>, WeightCfg<32>{})
-                   : launch(sea::pg::paged_weights_kernel<128>, WeightCfg<128>{});
+  const cudaError_t err = pl.rows == 16   ? launch(sea::pg::paged_weights_kernel<16>, WeightCfg<16>{})
+                          : pl.rows == 32 ? launch(sea::pg::paged_weights_kernel<32>, WeightCfg<32>{})
+                                          : launch(sea::pg::paged_weights_kernel<128>, WeightCfg<128>{});
+  if (err != cudaSuccess) return ATTN_ERR_CUDA;
+  if (pl.cluster == 0 && launch_pdl(sea::pg::paged_weights_merge_kernel, dim3(pl.ctas), dim3(sea::pg::BKV), 0, stream,
+                                    p) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  return ATTN_OK;
 }
 
 attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,

@@ -21,7 +21,9 @@
 // shares, one per resident CTA, so prompts (whose first slots more rows see) and
 // ragged batches come out even. A key tile whose items fall into several shares
 // leaves partial sums in the workspace, which paged_weights_merge_kernel adds in
-// the order of the line.
+// the order of the line. Where there are few key tiles with few items each, a
+// cluster of up to 8 CTAs takes one key tile, rank 0 adds the sums through
+// distributed shared memory, and there is no second launch and no workspace.
 //
 // Measured on a B200, 20 heads: one token of each of 16 sequences of 3.1 to 8.2
 // thousand slots 50 us = 4.7 TB/s (the loads run at 6.5 TB/s; 10 us are launch,
@@ -43,6 +45,7 @@ struct WeightParams {
   float scale_log2;
   fa::DivC dv_group;
   int tiles;           // key tiles per sequence, by the table's size
+  int cluster;         // 0: shares of the line; else so many CTAs, a cluster, per key tile
   float* ws_sum;       // [CTAs][2][128] sums of cut key tiles: one begun earlier, one that goes on
   int* ws_state;       // [CTAs][3]: the tile begun earlier ends or passes here; the entry of the one
                        // that goes on (-1: none), and in how many more shares
@@ -317,15 +320,27 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
   const WaitCtl wc{abort_flag, p.err, p.limit_ns};
 
   Located* found = reinterpret_cast<Located*>(smem + C::OFF_SCAN + 80);
-  locate(p, blockIdx.x, gridDim.x, C::THREADS, reinterpret_cast<long long*>(smem + C::OFF_SCAN), found);
   Share w;
   w.e.b = -1;
-  w.left = found->left;
-  const long long per = found->per;
-  if (w.left > 0) {
-    entry_at(p, w.e, found->b, found->tile);
-    w.i0 = found->i0;
+  long long per = 1;
+  int rank = 0;
+  if (p.cluster > 0) {
+    const int entry = blockIdx.x / p.cluster;
+    rank = blockIdx.x - entry * p.cluster;
+    const int b = entry / p.tiles;
+    entry_at(p, w.e, b, entry - b * p.tiles);
+    w.i0 = static_cast<int>(static_cast<long long>(w.e.items) * rank / p.cluster);
+    w.left = static_cast<int>(static_cast<long long>(w.e.items) * (rank + 1) / p.cluster) - w.i0;
     w.cut();
+  } else {
+    locate(p, blockIdx.x, gridDim.x, C::THREADS, reinterpret_cast<long long*>(smem + C::OFF_SCAN), found);
+    w.left = found->left;
+    per = found->per;
+    if (w.left > 0) {
+      entry_at(p, w.e, found->b, found->tile);
+      w.i0 = found->i0;
+      w.cut();
+    }
   }
 
   if (warp == C::WARPS && w.left > 0) {
@@ -437,6 +452,9 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     float* half_sum = reinterpret_cast<float*>(smem + C::OFF_HALF);
     int n = 0, entry_n = 0;
     int begun = 0, on = -1, more = 0;  // for the merge: see ws_state
+    // For rank 0, where the last query tile was: its products are done by then.
+    float* total = reinterpret_cast<float*>(smem + C::OFF_Q);
+    if (p.cluster > 1 && half == 0 && w.left <= 0) total[t] = 0.f;
     bool ok = true;
     if (w.left > 0) do {
     const int j = w.e.tile * BKV + t;
@@ -514,7 +532,9 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       ++entry_n;
       if (half == 1) continue;
     }
-    if (whole) {
+    if (p.cluster > 1) {
+      total[t] = sum;
+    } else if (whole) {
       if (j < g.cap) p.w_out[at] = w_old + sum;
     } else {
       const bool starts = w.i0 == 0;
@@ -527,7 +547,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       }
     }
     } while (ok && w.next(p));
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && p.cluster == 0) {
       p.ws_state[3 * blockIdx.x] = begun;
       p.ws_state[3 * blockIdx.x + 1] = on;
       p.ws_state[3 * blockIdx.x + 2] = more;
@@ -553,6 +573,24 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
+  if (p.cluster <= 1) return;
+  cluster_sync();
+  const int j = w.e.tile * BKV + static_cast<int>(threadIdx.x);
+  if (rank == 0 && threadIdx.x < BKV && w.e.items > 0 && j < g.cap) {
+    const uint32_t mine = sbase + C::OFF_Q + 4 * threadIdx.x;
+    const int64_t at = static_cast<int64_t>(w.e.b) * g.cap + j;
+    float part[8], v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      part[i] = 0.f;
+      if (i < p.cluster)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[i]) : "r"(mapa_shared(mine, i)) : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += part[i];
+    p.w_out[at] = (p.w_in != nullptr ? p.w_in[at] : 0.f) + v;
+  }
+  cluster_sync();  // no CTA leaves while rank 0 still reads its sums
 }
 
 // Adds up the key tiles that were cut: block c the one that begins in share c.

@@ -14,12 +14,16 @@ def make_cache(rng, lens, kv_heads, page, slots=None, spare=2, holes=(), garbage
     spare pages hold `garbage` (None: ordinary values); holes: (sequence, page
     index) entries set to -1. packed: K and V are column views of one buffer."""
     batch = len(lens)
-    slots = max(max(lens), 1) if slots is None else slots
+    longest = max(max(lens), 1)
+    slots = longest if slots is None else slots
     per_seq = -(-slots // page)
-    num_pages = batch * per_seq + spare
+    # a table much wider than the sequences has no pages behind their ends
+    backed = min(per_seq, -(-2 * longest // page))
+    num_pages = batch * backed + spare
     cols = kv_heads * D
     buf = torch.from_numpy(rng.standard_normal((num_pages * page, 2 * cols)).astype(np.float16))
-    table = rng.permutation(num_pages)[:batch * per_seq].reshape(batch, per_seq).astype(np.int32)
+    table = np.full((batch, per_seq), 2 ** 30, np.int32)
+    table[:, :backed] = rng.permutation(num_pages)[:batch * backed].reshape(batch, backed)
     for b, i in holes:
         table[b, i] = -1
     if garbage is not None:

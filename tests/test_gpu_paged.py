@@ -101,9 +101,12 @@ def test_attention_matches_the_oracle(name, slots):
     assert (big - dev(want)).abs().max() < 1e-12 and torch.equal(torch.isinf(big_lse), torch.isinf(dev(want_lse)))
 
 
+# Few slots per sequence: a CTA per key tile; many: shares of the line of items.
+@pytest.mark.parametrize("slots", [None, 80000])
 @pytest.mark.parametrize("name", [n for n in CASES if "sinks" not in n])
-def test_weights_match_the_oracle(name):
-    c, rng, cache, batch, q, opts, q_lens, _ = inputs(name)
+def test_weights_match_the_oracle(name, slots):
+    c, rng, cache, batch, q, opts, q_lens, _ = inputs(name, slots)
+    assert (attn.paged_weights_workspace_size(cache, batch, c["t_q"], c["heads"]) > 0) == (slots is not None)
     _, lse, _ = attention64(q, cache, c["t_q"], c["heads"], q_lens=q_lens, **opts)
     lse = lse.float().contiguous()
     w_in = torch.from_numpy(rng.random((batch, cache.slots)).astype(np.float32)).cuda()

@@ -78,7 +78,7 @@ def test_append_rejects_invalid_arguments(lib, kw):
 @pytest.mark.parametrize("kw", [
     dict(batch=0), dict(t_q=0), dict(heads=3), dict(q=m(Q, 100)), dict(lse=0), dict(lse=LSE + 2), dict(w_out=0),
     dict(w_out=W2 + 1), dict(w_in=W1 + 2), dict(w_in=W2 + 4), dict(w_out=Q), dict(w_out=LSE), dict(w_out=KP),
-    dict(scale=-1.0), dict(mk=mask(first=1)), dict(ws=0), dict(ws=WS + 4),
+    dict(scale=-1.0), dict(mk=mask(first=1)), dict(ws=0), dict(ws=WS + 4), dict(heads=2 * 129),
 ])
 def test_weights_rejects_invalid_arguments(lib, kw):
     st = lib.attn_paged_weights(kw.get("q", m(Q, 256)), cache(), kw.get("batch", 1), kw.get("t_q", 4),
@@ -113,6 +113,8 @@ def test_workspace_size_of_invalid_sizes_is_zero(lib):
     assert lib.attn_paged_workspace_size(cache(), 1, 0, 4, mask()) == 0
     assert lib.attn_paged_workspace_size(cache(n_kv_heads=3), 1, 1, 4, mask()) == 0
     assert lib.attn_paged_workspace_size(cache(n_kv_heads=1), 1, 1, 129, mask()) == 0
+    assert lib.attn_paged_weights_workspace_size(cache(), 0, 1, 4) == 0
+    assert lib.attn_paged_weights_workspace_size(cache(page_size=24), 1, 1, 4) == 0
 
 
 def test_binding_refuses_bad_caches():
