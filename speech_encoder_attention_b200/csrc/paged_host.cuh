@@ -268,7 +268,9 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   if (err != cudaSuccess) return ATTN_ERR_CUDA;
   if (pl.parts == 0) return ATTN_OK;
   const int unit_rows = pl.tok_per_tile * p.g.group;
-  const int rows_log2 = log2_of(std::min(unit_rows, 32));
+  // Fewer rows per block, and more groups of parts per row, where blocks are few.
+  int rows_log2 = log2_of(std::min(unit_rows, 32));
+  while (rows_log2 > 0 && units * ceil_div(unit_rows, 1 << rows_log2) < 2 * dev->num_sms) --rows_log2;
   if (launch_pdl(sea::pg::paged_combine_kernel,
                  dim3(static_cast<unsigned>(units), static_cast<unsigned>(ceil_div(unit_rows, 1 << rows_log2))),
                  dim3(sea::pg::COMBINE_THREADS), 0, stream, p, rows_log2) != cudaSuccess)
