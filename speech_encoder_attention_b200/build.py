@@ -12,8 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libattn.so")
-SOURCES = ["attn_api.cu"]
-HEADERS = ["attn_api.cu", "flash_attn.cuh", "paged_cache.cuh", "paged_chunk.cuh", "paged_common.cuh", "paged_host.cuh",
+SOURCES = ["paged_api.cu"]  # includes attn_api.cu
+HEADERS = ["attn_api.cu", "flash_attn.cuh", "paged_api.cu", "paged_cache.cuh", "paged_chunk.cuh", "paged_common.cuh",
            "paged_step.cuh", "paged_weights.cuh", "qkv_gemm.cuh", "qkv_q8.cuh", "sm100_ptx.cuh"]
 
 

@@ -16,11 +16,6 @@
 
 #include "attn.h"
 #include "flash_attn.cuh"
-#include "paged_cache.cuh"
-#include "paged_chunk.cuh"
-#include "paged_common.cuh"
-#include "paged_step.cuh"
-#include "paged_weights.cuh"
 #include "qkv_gemm.cuh"
 #include "qkv_q8.cuh"
 #include "sm100_ptx.cuh"
@@ -104,15 +99,6 @@ auto narrow_attention_kernel(bool ext) {
   return ext ? sea::fa::flash_attn_kernel<false, true, 4, true> : sea::fa::flash_attn_kernel<false, false, 4, true>;
 }
 
-template <int MT>
-bool set_paged_step_smem() {
-  constexpr int bytes = sea::pg::StepCfg<MT>::SMEM_BYTES;
-  return cudaFuncSetAttribute(sea::pg::paged_step_kernel<MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              bytes) == cudaSuccess &&
-         cudaFuncSetAttribute(sea::pg::paged_step_kernel<MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              bytes) == cudaSuccess;
-}
-
 // Per-device set-up: checks for an sm_100 part, records the SM count and the
 // error-word address, and raises the dynamic shared-memory limits once.
 attn_status device_info(DeviceInfo** out) {
@@ -141,15 +127,6 @@ attn_status device_info(DeviceInfo** out) {
                              sea::gemm::PairShape::SMEM_BYTES) != cudaSuccess ||
         cudaFuncSetAttribute(sea::q8::qkv_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              sea::q8::SMEM_BYTES) != cudaSuccess ||
-        !set_paged_step_smem<1>() || !set_paged_step_smem<2>() ||
-        cudaFuncSetAttribute(sea::pg::paged_weights_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sea::pg::WeightCfg<16>::SMEM_BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(sea::pg::paged_weights_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sea::pg::WeightCfg<32>::SMEM_BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(sea::pg::paged_weights_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sea::pg::WeightCfg<128>::SMEM_BYTES) != cudaSuccess ||
-        cudaFuncSetAttribute(sea::pg::paged_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             sea::pg::ChunkCfg::SMEM_BYTES) != cudaSuccess ||
         !set_attention_smem<2>() || !set_attention_smem<4>())
       return ATTN_ERR_CUDA;
     d.num_sms = sms;
@@ -536,8 +513,6 @@ attn_status static_scratch(void** out) {
   return ATTN_OK;
 }
 
-#include "paged_host.cuh"
-
 }  // namespace
 
 extern "C" {
@@ -687,46 +662,6 @@ size_t attn_workspace_size(int32_t batch, int32_t t_q, int32_t t_kv, int32_t n_h
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != ATTN_OK) return 0;
   return plan_forward(batch, t_q, t_kv, n_heads, mask_kind, 0, dev->num_sms).ws_bytes;
-}
-
-attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cache, int32_t batch, int32_t t_new,
-                              const int32_t* q_lens, attn_stream_t stream) {
-  return launch_paged_append(k_new, v_new, cache, batch, t_new, q_lens, stream);
-}
-
-attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
-                       attn_paged_mask mask, const float* sinks, float scale, attn_mat out, float* lse,
-                       void* workspace, size_t workspace_bytes, attn_stream_t stream) {
-  return launch_paged(q, cache, batch, t_q, n_heads, mask, sinks, scale, out, lse, workspace, workspace_bytes, stream);
-}
-
-size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
-                                 attn_paged_mask mask) {
-  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch) ||
-      !valid_paged_mask(mask))
-    return 0;
-  DeviceInfo* dev = nullptr;
-  if (device_info(&dev) != ATTN_OK) return 0;
-  return plan_paged(paged_geo(cache, batch, t_q, n_heads, mask), dev->num_sms).ws_bytes;
-}
-
-size_t attn_paged_weights_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads) {
-  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch)) return 0;
-  DeviceInfo* dev = nullptr;
-  if (device_info(&dev) != ATTN_OK) return 0;
-  return plan_weights(paged_geo(cache, batch, t_q, n_heads, attn_paged_mask{}), dev->num_sms).ws_bytes;
-}
-
-attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
-                               attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
-                               void* workspace, size_t workspace_bytes, attn_stream_t stream) {
-  return launch_paged_weights(q, cache, batch, t_q, n_heads, mask, lse, scale, w_in, w_out, workspace,
-                              workspace_bytes, stream);
-}
-
-attn_status attn_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,
-                             const float* w_in, attn_paged_kv dst, float* w_out, int32_t* kept, attn_stream_t stream) {
-  return launch_paged_evict(cache, batch, budget, first, recent, w_in, dst, w_out, kept, stream);
 }
 
 const char* attn_status_string(attn_status status) {

@@ -1,6 +1,43 @@
-// paged_host.cuh -- host side of the paged-cache entry points: argument
-// checks (pure arithmetic, before any CUDA call), launch plans and launches.
-// Included by attn_api.cu inside its unnamed namespace.
+// paged_api.cu -- the translation unit of libattn.so: attn_api.cu, whose helpers
+// serve here too, and the C ABI's paged-cache entry points. Host side of those:
+// argument checks (pure arithmetic, before any CUDA call), launch plans and
+// launches.
+#include "attn_api.cu"
+
+#include "paged_cache.cuh"
+#include "paged_chunk.cuh"
+#include "paged_common.cuh"
+#include "paged_step.cuh"
+#include "paged_weights.cuh"
+
+namespace {
+
+bool g_paged_init[kMaxDevices] = {};
+
+template <typename Kernel>
+bool set_smem(Kernel* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+// device_info, and once per device the paged kernels' shared-memory limits.
+attn_status paged_device(DeviceInfo** out) {
+  if (attn_status st = device_info(out); st != ATTN_OK) return st;
+  const auto dev = *out - g_dev;
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (g_paged_init[dev]) return ATTN_OK;
+  using namespace sea::pg;
+  if (!set_smem(paged_step_kernel<1, false>, StepCfg<1>::SMEM_BYTES) ||
+      !set_smem(paged_step_kernel<1, true>, StepCfg<1>::SMEM_BYTES) ||
+      !set_smem(paged_step_kernel<2, false>, StepCfg<2>::SMEM_BYTES) ||
+      !set_smem(paged_step_kernel<2, true>, StepCfg<2>::SMEM_BYTES) ||
+      !set_smem(paged_chunk_kernel, ChunkCfg::SMEM_BYTES) ||
+      !set_smem(paged_weights_kernel<16>, WeightCfg<16>::SMEM_BYTES) ||
+      !set_smem(paged_weights_kernel<32>, WeightCfg<32>::SMEM_BYTES) ||
+      !set_smem(paged_weights_kernel<128>, WeightCfg<128>::SMEM_BYTES))
+    return ATTN_ERR_CUDA;
+  g_paged_init[dev] = true;
+  return ATTN_OK;
+}
 
 constexpr int kMaxGroup = 128; // query heads per K/V head
 
@@ -172,7 +209,7 @@ attn_status launch_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv ca
     if (overlaps(r, pool_range(cache, cache.k)) || overlaps(r, pool_range(cache, cache.v))) return ATTN_ERR_INVALID;
   }
   DeviceInfo* dev = nullptr;
-  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  if (attn_status st = paged_device(&dev); st != ATTN_OK) return st;
   sea::pg::AppendParams p{};
   attn_paged_mask none{};
   none.q_lens = q_lens;
@@ -210,7 +247,7 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   if (!aligned16(workspace) || (workspace == nullptr && workspace_bytes != 0)) return ATTN_ERR_INVALID;
 
   DeviceInfo* dev = nullptr;
-  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  if (attn_status st = paged_device(&dev); st != ATTN_OK) return st;
   sea::pg::StepParams p{};
   p.g = paged_geo(cache, batch, t_q, n_heads, mask);
   const PagedPlan pl = plan_paged(p.g, dev->num_sms);
@@ -337,7 +374,7 @@ attn_status launch_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch,
   if (!aligned16(workspace) || (workspace == nullptr && workspace_bytes != 0)) return ATTN_ERR_INVALID;
 
   DeviceInfo* dev = nullptr;
-  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  if (attn_status st = paged_device(&dev); st != ATTN_OK) return st;
   sea::pg::WeightParams p{};
   p.g = paged_geo(cache, batch, t_q, n_heads, mask);
   const WeightPlan pl = plan_weights(p.g, dev->num_sms);
@@ -404,7 +441,7 @@ attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budge
         if (overlaps(pool_range(cache, a), pool_range(dst, b))) return ATTN_ERR_INVALID;
 
   DeviceInfo* dev = nullptr;
-  if (attn_status st = device_info(&dev); st != ATTN_OK) return st;
+  if (attn_status st = paged_device(&dev); st != ATTN_OK) return st;
   sea::pg::EvictParams p{};
   p.g = paged_geo(cache, batch, 1, cache.n_kv_heads, attn_paged_mask{});
   p.budget = budget;
@@ -444,3 +481,49 @@ attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budge
     return ATTN_ERR_CUDA;
   return ATTN_OK;
 }
+
+}  // namespace
+
+extern "C" {
+
+attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cache, int32_t batch, int32_t t_new,
+                              const int32_t* q_lens, attn_stream_t stream) {
+  return launch_paged_append(k_new, v_new, cache, batch, t_new, q_lens, stream);
+}
+
+attn_status attn_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                       attn_paged_mask mask, const float* sinks, float scale, attn_mat out, float* lse,
+                       void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  return launch_paged(q, cache, batch, t_q, n_heads, mask, sinks, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                                 attn_paged_mask mask) {
+  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch) ||
+      !valid_paged_mask(mask))
+    return 0;
+  DeviceInfo* dev = nullptr;
+  if (paged_device(&dev) != ATTN_OK) return 0;
+  return plan_paged(paged_geo(cache, batch, t_q, n_heads, mask), dev->num_sms).ws_bytes;
+}
+
+size_t attn_paged_weights_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads) {
+  if (!valid_paged_heads(batch, t_q, n_heads, cache.n_kv_heads) || !valid_cache(cache, batch)) return 0;
+  DeviceInfo* dev = nullptr;
+  if (paged_device(&dev) != ATTN_OK) return 0;
+  return plan_weights(paged_geo(cache, batch, t_q, n_heads, attn_paged_mask{}), dev->num_sms).ws_bytes;
+}
+
+attn_status attn_paged_weights(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t t_q, int32_t n_heads,
+                               attn_paged_mask mask, const float* lse, float scale, const float* w_in, float* w_out,
+                               void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+  return launch_paged_weights(q, cache, batch, t_q, n_heads, mask, lse, scale, w_in, w_out, workspace,
+                              workspace_bytes, stream);
+}
+
+attn_status attn_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budget, int32_t first, int32_t recent,
+                             const float* w_in, attn_paged_kv dst, float* w_out, int32_t* kept, attn_stream_t stream) {
+  return launch_paged_evict(cache, batch, budget, first, recent, w_in, dst, w_out, kept, stream);
+}
+
+}  // extern "C"
