@@ -135,6 +135,9 @@ LARGE = {
     "many": dict(lens=[5 + 37 * i % 400 for i in range(70)], t_q=2, heads=8, kv=4, page=16),
     "prompt_many": dict(lens=[max(i % 7 * 50, i * 37 % 300) for i in range(31)], t_q=200, heads=20, kv=20, page=64,
                         q_lens=[min(200, max(i % 7 * 50, i * 37 % 300)) for i in range(31)]),
+    "many_cut": dict(lens=[5 + 37 * i % 400 for i in range(70)], t_q=2, heads=8, kv=4, page=16, slots=14000),
+    "one_cut": dict(lens=[13999, 12001], t_q=1, heads=8, kv=2, page=64, slots=14000),
+    "chunk_many_cut": dict(lens=[150 + 37 * i % 400 for i in range(40)], t_q=140, heads=2, kv=1, page=16, slots=4000),
     "chunk_many": dict(lens=[150 + 37 * i % 400 for i in range(40)], t_q=140, heads=2, kv=1, page=16),
 }
 
@@ -144,7 +147,7 @@ def test_large_attention_and_weights(name):
     c = LARGE[name]
     rng = np.random.default_rng(len(name))
     batch = len(c["lens"])
-    cache = make_cache(rng, c["lens"], c["kv"], c["page"], garbage=NAN)
+    cache = make_cache(rng, c["lens"], c["kv"], c["page"], garbage=NAN, slots=c.get("slots"))
     q = queries(rng, batch, c["t_q"], c["heads"])
     q_lens = c.get("q_lens")
     opts = dict(window=c.get("window", 0), first=c.get("first", 0), causal=c.get("causal", True))
@@ -444,3 +447,90 @@ def test_numbers_that_do_not_fit_are_refused():
         attn.attn_paged(q, cache, 1, 1, 1, first=3)
     with pytest.raises(attn.AttnError):
         attn.attn_paged_evict(cache, torch.zeros(1, 32, device="cuda"), 33)
+
+
+@pytest.mark.parametrize("t_q", [1, 20, 50])
+def test_lengths_out_of_range_are_clamped(t_q):
+    rng = np.random.default_rng(19)
+    cache = make_cache(rng, [96, 96, 96], 2, 16)
+    q = queries(rng, 3, t_q, 4)
+    wild = attn.PagedKV(cache.k, cache.v, cache.table, i32([2 ** 31 - 1, -5, 50]), 16, 2)
+    tame = attn.PagedKV(cache.k, cache.v, cache.table, i32([96, 0, 50]), 16, 2)
+    got, lse = attn.attn_paged(q, wild, 3, t_q, 4, q_lens=i32([2 ** 31 - 1, 3, -(2 ** 31)]), return_lse=True)
+    want, want_lse = attn.attn_paged(q, tame, 3, t_q, 4, q_lens=i32([t_q, 3, 0]), return_lse=True)
+    assert torch.equal(got, want) and torch.equal(lse, want_lse) and (got[t_q:] == 0).all()
+    w = attn.attn_paged_weights(q, wild, lse, 3, t_q, 4, q_lens=i32([2 ** 31 - 1, 3, -(2 ** 31)]))
+    assert torch.equal(w, attn.attn_paged_weights(q, tame, lse, 3, t_q, 4, q_lens=i32([t_q, 3, 0])))
+
+
+@pytest.mark.parametrize("t_q", [1, 40])
+def test_sequences_may_share_pages(t_q):
+    """A common prefix held once, and one page twice in a row."""
+    rng = np.random.default_rng(20)
+    cache = make_cache(rng, [200, 160, 90], 2, 16)
+    cache.table[1, :6] = cache.table[0, :6]
+    cache.table[2, 3] = cache.table[2, 2]
+    q = queries(rng, 3, t_q, 4)
+    got, lse = attn.attn_paged(q, cache, 3, t_q, 4, return_lse=True)
+    check_attention(got, lse, *attention64(q, cache, t_q, 4), 200)
+    zero = torch.zeros(3, cache.slots, device="cuda")
+    w = attn.attn_paged_weights(q, cache, lse, 3, t_q, 4, weights=zero)
+    check_weights(w, weights64(q, cache, lse, t_q, 4, zero), zero)
+
+
+def test_captured_eviction_follows_its_inputs():
+    rng = np.random.default_rng(21)
+    cache = make_cache(rng, [300, 300], 2, 16)
+    w = torch.zeros(2, cache.slots, device="cuda")
+    kept = torch.empty(2, 64, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        attn.attn_paged_evict(cache, w, 64, 2, 10, kept=kept, weights_out=w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.attn_paged_evict(cache, w, 64, 2, 10, kept=kept, weights_out=w)
+    for lens in ([300, 100], [64, 65], [0, 299]):
+        cache.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        w.copy_(torch.from_numpy(rng.random((2, cache.slots)).astype(np.float32)))
+        k, v, table, ln = parts(cache)
+        want = oracle.evict(k, v, table, ln, w.cpu().numpy(), 16, 64, 2, 10, k, v, table)
+        graph.replay()
+        for g, x in zip((cache.k, cache.v, kept, cache.lens, w), want):
+            assert np.array_equal(g.cpu().numpy(), x)
+
+
+def test_everything_at_once_on_three_streams():
+    """Appends, attention, weights and evictions of unrelated caches overlap."""
+    rng = np.random.default_rng(22)
+
+    def job(i, stream):
+        cache = caches[i]
+        attn.attn_paged_append(q[i], q[i], cache, 2, 1 + 40 * i, stream=stream)
+        out, lse = attn.attn_paged(q[i], cache, 2, 1 + 40 * i, 4, return_lse=True, stream=stream)
+        w = attn.attn_paged_weights(q[i], cache, lse, 2, 1 + 40 * i, 4, stream=stream)
+        kept, w2 = attn.attn_paged_evict(cache, w, 500, 4, 100, stream=stream)
+        return out, lse, w, kept, w2, cache.k.clone(), cache.v.clone(), cache.lens.clone()
+
+    base = [make_cache(rng, [2000 + i, 1700], 4, 64, slots=16000 if i == 1 else None) for i in range(3)]
+    q = [queries(rng, 2, 1 + 40 * i, 4) for i in range(3)]
+
+    def fresh():
+        return [attn.PagedKV(c.k.clone(), c.v.clone(), c.table, c.lens.clone(), 64, 4) for c in base]
+
+    caches = fresh()
+    alone = []
+    for i in range(3):
+        alone.append(job(i, None))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(3):
+        caches = fresh()
+        torch.cuda.synchronize()
+        got = [None] * 3
+        for i in range(3):
+            with torch.cuda.stream(streams[i]):  # the clones at the end belong to the stream too
+                got[i] = job(i, streams[i])
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
