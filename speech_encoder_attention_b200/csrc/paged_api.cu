@@ -464,9 +464,10 @@ attn_status launch_paged_evict(attn_paged_kv cache, int32_t batch, int32_t budge
   p.k_out_stride = dst.k.row_stride;
   p.v_out_stride = dst.v.row_stride;
   int ranks = 1;
-  while (ranks < 8 && static_cast<int64_t>(ranks) * sea::pg::SELECT_THREADS < cap) ranks *= 2;
-  if (launch_pdl_cluster(sea::pg::paged_select_kernel, dim3(ranks, batch), dim3(sea::pg::SELECT_THREADS), 0, stream,
-                         static_cast<unsigned>(ranks), p) != cudaSuccess)
+  while (ranks < 8 && ranks * int64_t(1024) < cap) ranks *= 2;
+  const int threads = ranks == 1 ? 512 : 1024;
+  if (launch_pdl_cluster(ranks == 1 ? sea::pg::paged_select_kernel<512> : sea::pg::paged_select_kernel<1024>,
+                         dim3(ranks, batch), dim3(threads), 0, stream, static_cast<unsigned>(ranks), p) != cudaSuccess)
     return ATTN_ERR_CUDA;
   // Other pools: CTAs of a few whole rows, one step each, in any order, so that
   // a row's bytes are read together. The same pool: a CTA per head's columns,

@@ -93,8 +93,9 @@ __device__ __forceinline__ uint32_t evict_key(const EvictParams& p, const Seq& s
 // Select: a cluster of up to 8 CTAs per sequence, each with an equal run of its
 // slots. Bound by latency: a pass costs a histogram in shared memory, a cluster
 // barrier and 8 remote reads per digit, so the keys are computed once (8192 of
-// a CTA's stay in shared memory; longer runs recompute the rest).
-constexpr int SELECT_THREADS = 1024;
+// a CTA's stay in shared memory; longer runs recompute the rest). One CTA alone
+// (up to 1024 slots) is quicker with 512 threads, whose barriers are cheaper
+// (five caches of up to 448 slots: 9.6 against 11.0 us with the move).
 constexpr int SELECT_CACHED = 8192;
 
 __device__ __forceinline__ uint32_t ld_shared_cluster_u32(const uint32_t* mine, uint32_t rank) {
@@ -103,6 +104,7 @@ __device__ __forceinline__ uint32_t ld_shared_cluster_u32(const uint32_t* mine, 
   return v;
 }
 
+template <int SELECT_THREADS>
 __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const EvictParams p) {
   __shared__ uint32_t keys[SELECT_CACHED];
   __shared__ uint32_t hist[2][256];          // by pass, so one cluster barrier per pass is enough
@@ -113,6 +115,7 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int rank = blockIdx.x, ranks = gridDim.x, b = blockIdx.y;
   if (t < 512) hist[t >> 8][t & 255] = 0u;
+  if (t < 32) warp_sum[t] = warp_eq[t] = 0u;
   griddep_wait();
   griddep_launch_dependents();
   const Seq s = seq_of(p.g, b);
@@ -120,7 +123,6 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
   const int run = (s.kv + ranks - 1) / ranks;
   const int ja = min(s.kv, rank * run), jz = min(s.kv, ja + run);
   auto key_at = [&](int j) { return j - ja < SELECT_CACHED ? keys[j - ja] : evict_key(p, s, b, j, w); };
-  for (int j = ja + t; j < min(jz, ja + SELECT_CACHED); j += SELECT_THREADS) keys[j - ja] = evict_key(p, s, b, j, w);
   __syncthreads();
 
   // The budget-th largest key, digit by digit from the top: kept are the keys
@@ -134,7 +136,11 @@ __global__ void __launch_bounds__(SELECT_THREADS, 1) paged_select_kernel(const E
     uint32_t* h = hist[pass & 1];
     for (int j0 = ja; j0 < jz; j0 += SELECT_THREADS) {
       const int j = j0 + t;
-      const uint32_t key = j < jz ? key_at(j) : 0u;
+      uint32_t key = 0u;
+      if (j < jz) {
+        key = pass == 0 ? evict_key(p, s, b, j, w) : key_at(j);
+        if (pass == 0 && j - ja < SELECT_CACHED) keys[j - ja] = key;
+      }
       const bool in = key != 0u && (pass == 0 || (key >> (shift + 8)) == prefix);
       const uint32_t digit = in ? (key >> shift) & 255u : 256u;
       const uint32_t same = __match_any_sync(0xffffffffu, digit);  // equal digits of a warp count once
