@@ -6,7 +6,9 @@
 // With few query rows bound by reading K; with many, by one exponential per
 // (row, head, slot). A CTA owns 128 slots of one sequence and computes
 // S^T = K Q^T on tcgen05 tiles: 128 slots x N rows, N = 16 or 32 for a step or
-// a drafted block, 128 for a longer chunk. A slot is a tensor-memory lane, so its
+// a drafted block, 128 for a longer chunk (20 heads, us: a step over 1500 slots of
+// five sequences 8.2 with 16, 8.6 with 32; 24 rows of those 8.9 with 32, 18.3 with
+// 128). A slot is a tensor-memory lane, so its
 // weights are summed by one thread, in a fixed order, with no shuffles; the
 // normaliser of a row is a column's constant that every thread reads from
 // shared memory.
@@ -60,7 +62,10 @@ struct WeightCfg {
   static constexpr int NC = N / SPLIT;            // columns of a thread
   static constexpr int WARPS = 4 * SPLIT;
   static constexpr int THREADS = 32 * (WARPS + 2);
-  static constexpr int K_STAGES = N == 128 ? 2 : 3;
+  // Four CTAs per SM hide each other's waits; a third K stage fits them beside 16
+  // rows only (32 rows of 16 x 8000 slots, us: three CTAs of three stages 68, of
+  // four stages 66, four of two 65).
+  static constexpr int K_STAGES = N == 16 ? 3 : 2;
   static constexpr int Q_STAGES = 3;
   static constexpr int CTAS_PER_SM = N == 128 ? 2 : 4;
   static constexpr int Q_BYTES = N * DH * 2;
@@ -75,6 +80,7 @@ struct WeightCfg {
   static constexpr int OFF_HALF = OFF_SCAN + 8 * 10 + 32;   // [128] the second half's sums
   static constexpr int OFF_MISC = OFF_HALF + (SPLIT == 2 ? BKV * 4 : 0);
   static constexpr int SMEM_BYTES = 1024 + OFF_MISC + 16;
+  static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "the CTAs of an SM do not fit it together");
 };
 
 template <int N>
