@@ -139,12 +139,19 @@ bool encode_paged_q(CUtensorMap* m, const attn_mat& q, int batch, int t_q, int n
          CUDA_SUCCESS;
 }
 
-// Chunks with at least this many units per CTA, or with at most this many key
-// tiles per unit, are walked unit by unit; the others are cut into equal shares.
-// 20 heads, us: 8 prompts of 1500 tokens 113 by units, 155 cut; 100 tokens after
-// 448 slots 11.7 by units, 15.7 cut, after 1500 slots 23.0 and 22.8.
-constexpr int kWholeUnitsPerCta = 4;
-constexpr int kWholeChunkTiles = 8;
+// A chunk's units are walked whole, not cut into equal parts, where the longest SM
+// works at most kCutTiles key tiles and kCutShare of the mean beyond the mean, which
+// is what partials, their merging and the parts' uneven unit ends cost. An SM has two
+// units at a time; an odd one left alone takes kAloneTile of a pair's time. Longest
+// first, causal units of different lengths even out by themselves. 20 heads,
+// us: 8 prompts of 1500 tokens 113 whole, 155 cut; one of 6000 150 and 186; 100
+// tokens after 448 slots 11.7 and 15.7, after 1500 slots 23.0 and 17.5; 4 chunks of
+// 500 tokens at the end of 6000 slots 178 and 132. Over 894 sizes of 40 to 4000
+// tokens and up to 12000 slots the choice costs 0.5 % on average against the better
+// of both, at most 25 %.
+constexpr float kAloneTile = 0.7f;
+constexpr float kCutTiles = 5.5f;
+constexpr float kCutShare = 0.1f;
 
 // A unit of paged_step_kernel gets a cluster of its own instead of being cut into
 // parts where a CTA of it has at most kClusterStepTiles key tiles, and a single CTA
@@ -178,7 +185,8 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
   const int64_t units = int64_t(g.batch) * kv_heads * pl.q_tiles;
   // The cache bounds a unit's key tiles, or the window (its other side too
   // unless causal), whose ends fall inside tiles, and the first tokens.
-  int64_t tiles = ceil_div(g.cap, sea::pg::BKV);
+  const int64_t cap_tiles = ceil_div(g.cap, sea::pg::BKV);
+  int64_t tiles = cap_tiles;
   if (g.window > 0) {
     const int64_t reach = int64_t(g.causal ? 1 : 2) * g.window + pl.tok_per_tile;
     tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
@@ -193,10 +201,17 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
       pl.ctas = static_cast<int>(units * cluster);
       return pl;
     }
-  } else if (tiles <= kWholeChunkTiles || units >= int64_t(kWholeUnitsPerCta) * 2 * num_sms) {
-    pl.parts = 0;
-    pl.ctas = static_cast<int>(std::min<int64_t>(units, int64_t(2) * num_sms));
-    return pl;
+  } else {
+    const int64_t sm_units = (units + num_sms - 1) / num_sms;
+    const float longest = static_cast<float>(tiles) * (sm_units / 2 + (sm_units % 2 != 0 ? kAloneTile : 0.f));
+    const float mean = static_cast<float>(tiles) * units / (2 * num_sms);
+    float beyond = longest - mean;
+    if (g.causal && tiles == cap_tiles) beyond *= 1.f - std::min(1.f, float(t_q) / g.cap);
+    if (beyond <= kCutTiles + kCutShare * mean) {
+      pl.parts = 0;
+      pl.ctas = static_cast<int>(std::min<int64_t>(units, int64_t(2) * num_sms));
+      return pl;
+    }
   }
   pl.ws_bytes = size_t(2) * pl.ctas * pl.rows_cap * (sea::pg::DH * sizeof(float) + sizeof(float2));
   return pl;

@@ -138,6 +138,7 @@ LARGE = {
     "many_cut": dict(lens=[5 + 37 * i % 400 for i in range(70)], t_q=2, heads=8, kv=4, page=16, slots=14000),
     "one_cut": dict(lens=[13999, 12001], t_q=1, heads=8, kv=2, page=64, slots=14000),
     "chunk_many_cut": dict(lens=[150 + 37 * i % 400 for i in range(40)], t_q=140, heads=2, kv=1, page=16, slots=4000),
+    "chunk_cut": dict(lens=[6001, 900, 2509], t_q=300, heads=20, kv=4, page=128, q_lens=[300, 300, 41]),
     "chunk_many": dict(lens=[150 + 37 * i % 400 for i in range(40)], t_q=140, heads=2, kv=1, page=16),
 }
 
@@ -151,6 +152,7 @@ def test_large_attention_and_weights(name):
     q = queries(rng, batch, c["t_q"], c["heads"])
     q_lens = c.get("q_lens")
     opts = dict(window=c.get("window", 0), first=c.get("first", 0), causal=c.get("causal", True))
+    assert "cut" not in name or attn.paged_workspace_size(cache, batch, c["t_q"], c["heads"], **opts) > 0
     got, lse = attn.attn_paged(q, cache, batch, c["t_q"], c["heads"], q_lens=i32(q_lens), return_lse=True, **opts)
     want, want_lse, spread = attention64(q, cache, c["t_q"], c["heads"], q_lens=q_lens, **opts)
     check_attention(got, lse, want, want_lse, spread, max(c["lens"]))
