@@ -153,13 +153,40 @@ constexpr float kAloneTile = 0.7f;
 constexpr float kCutTiles = 5.5f;
 constexpr float kCutShare = 0.1f;
 
-// A unit of paged_step_kernel gets a cluster of its own instead of being cut into
-// parts where a CTA of it has at most kClusterStepTiles key tiles, and a single CTA
-// up to kCtaStepTiles. One token, 20 heads, us per step: a CTA 4.5 at 128 slots,
-// 6.5 at 448, 7.8 at 768, 11.9 at 1500; a cluster of eight 7.6 at 1500, 8.2 at
-// 3000, 17.1 at 12000; cut parts 10.3 at 448, 12.2 at 3000, 19.6 at 12000.
-constexpr int kCtaStepTiles = 6;
-constexpr int kClusterStepTiles = 12;
+// A unit of paged_step_kernel gets a CTA, or a cluster of 2 to 8, or is cut with all
+// others into equal parts, whichever the estimate below says is quicker, in key tiles
+// of an SM's two CTAs, which read as fast as the memory allows: a CTA takes at least
+// kLoneTile of that per tile, a cluster kClusterTiles to merge, cut parts kMergeTiles.
+// Where a CTA would have more than kMostTiles the units are cut all the same: with
+// lengths far apart equal parts are safer. One token, 20 heads, us: a CTA 4.7 at 128
+// slots, 6.6 at 448, 8.0 at 700, 12.3 at 1500; a cluster of eight 7.0 at 700, 7.6 at
+// 1500, 8.3 at 3000; cut parts 10.8 at 700, 11.4 at 1500, 12.3 at 3000. Over 699 sizes
+// of 1 to 64 sequences, 1 to 20 K/V heads and up to 12000 slots the choice costs
+// 1 % on average against the best of all, at most 18 %.
+constexpr float kLoneTile = 0.55f;
+constexpr float kClusterTiles = 1.75f;
+constexpr float kMergeTiles = 6.f;
+constexpr int kMostTiles = 24;
+
+// CTAs per unit of `tiles` key tiles; 0: cut.
+int plan_step_cluster(int64_t units, int64_t tiles, int num_sms) {
+  const int64_t slots = int64_t(2) * num_sms;
+  float least = kMergeTiles + static_cast<float>(tiles) * units / slots;
+  int best = 0;
+  for (int c = 1; c <= 8 && (c == 1 || units * c <= slots); c *= 2) {
+    const int64_t run = (tiles + c - 1) / c;
+    if (run > kMostTiles) continue;
+    const int64_t rest = units * c % slots;
+    float waves = static_cast<float>(units * c / slots);
+    if (rest != 0) waves += std::max(kLoneTile, static_cast<float>(rest) / slots);
+    const float cost = run * waves + (c > 1 ? kClusterTiles : 0.f);
+    if (cost < least) {
+      least = cost;
+      best = c;
+    }
+  }
+  return best;
+}
 
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
@@ -192,10 +219,8 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
     tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
   }
   if (pl.rows_cap <= 32) {
-    int cluster = 1;
-    if (tiles > kCtaStepTiles)
-      while (cluster < 8 && units * 2 * cluster <= 2 * num_sms) cluster *= 2;
-    if (tiles <= int64_t(kClusterStepTiles) * cluster) {
+    const int cluster = plan_step_cluster(units, tiles, num_sms);
+    if (cluster > 0) {
       pl.parts = 0;
       pl.cluster = cluster;
       pl.ctas = static_cast<int>(units * cluster);

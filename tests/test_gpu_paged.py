@@ -136,6 +136,8 @@ LARGE = {
     "prompt_many": dict(lens=[max(i % 7 * 50, i * 37 % 300) for i in range(31)], t_q=200, heads=20, kv=20, page=64,
                         q_lens=[min(200, max(i % 7 * 50, i * 37 % 300)) for i in range(31)]),
     "many_cut": dict(lens=[5 + 37 * i % 400 for i in range(70)], t_q=2, heads=8, kv=4, page=16, slots=14000),
+    "four": dict(lens=[1000, 300, 700], t_q=1, heads=20, kv=20, page=32),
+    "two_waves": dict(lens=[200 + 31 * i % 300 for i in range(18)], t_q=1, heads=20, kv=20, page=16),
     "one_cut": dict(lens=[13999, 12001], t_q=1, heads=8, kv=2, page=64, slots=14000),
     "chunk_many_cut": dict(lens=[150 + 37 * i % 400 for i in range(40)], t_q=140, heads=2, kv=1, page=16, slots=4000),
     "chunk_cut": dict(lens=[6001, 900, 2509], t_q=300, heads=20, kv=4, page=128, q_lens=[300, 300, 41]),
