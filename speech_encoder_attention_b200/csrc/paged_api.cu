@@ -153,33 +153,30 @@ constexpr float kAloneTile = 0.7f;
 constexpr float kCutTiles = 5.5f;
 constexpr float kCutShare = 0.1f;
 
-// A unit of paged_step_kernel gets a CTA, or a cluster of 2 to 8, or is cut with all
-// others into equal parts, whichever the estimate below says is quicker, in key tiles
-// of an SM's two CTAs, which read as fast as the memory allows: a CTA takes at least
-// kLoneTile of that per tile, a cluster kClusterTiles to merge, cut parts kMergeTiles.
-// Where a CTA would have more than kMostTiles the units are cut all the same: with
-// lengths far apart equal parts are safer. One token, 20 heads, us: a CTA 4.7 at 128
-// slots, 6.6 at 448, 8.0 at 700, 12.3 at 1500; a cluster of eight 7.0 at 700, 7.6 at
-// 1500, 8.3 at 3000; cut parts 10.8 at 700, 11.4 at 1500, 12.3 at 3000. Over 699 sizes
-// of 1 to 64 sequences, 1 to 20 K/V heads and up to 12000 slots the choice costs
-// 1 % on average against the best of all, at most 18 %.
-constexpr float kLoneTile = 0.55f;
-constexpr float kClusterTiles = 1.75f;
-constexpr float kMergeTiles = 6.f;
-constexpr int kMostTiles = 24;
+// Units of `run` tiles each go to a CTA each, or to a cluster of 2 to 8 that shares
+// the unit's tiles, or all are cut into equal parts, one per resident CTA, and merged:
+// whichever the estimate below says is quicker, in tiles of a full device. What it
+// leaves out: lengths may be far below the cache's size, or far apart, where equal
+// parts are safer; so a CTA gets at most `most` tiles, or the units are cut.
+struct SplitCosts {
+  float lone;   // time of a tile where few CTAs run
+  float setup;  // of a CTA
+  float merge;  // of a cluster
+  float cut;    // of cut parts: partials and a second kernel
+  int most;
+};
 
-// CTAs per unit of `tiles` key tiles; 0: cut.
-int plan_step_cluster(int64_t units, int64_t tiles, int num_sms) {
-  const int64_t slots = int64_t(2) * num_sms;
-  float least = kMergeTiles + static_cast<float>(tiles) * units / slots;
+// CTAs per unit; 0: cut.
+int plan_split(int64_t units, int64_t run, int64_t resident, const SplitCosts& costs) {
+  float least = costs.cut + costs.setup + static_cast<float>(run) * units / resident;
   int best = 0;
-  for (int c = 1; c <= 8 && (c == 1 || units * c <= slots); c *= 2) {
-    const int64_t run = (tiles + c - 1) / c;
-    if (run > kMostTiles) continue;
-    const int64_t rest = units * c % slots;
-    float waves = static_cast<float>(units * c / slots);
-    if (rest != 0) waves += std::max(kLoneTile, static_cast<float>(rest) / slots);
-    const float cost = run * waves + (c > 1 ? kClusterTiles : 0.f);
+  for (int c = 1; c <= 8 && (c == 1 || units * c <= resident); c *= 2) {
+    const int64_t own = (run + c - 1) / c;
+    if (own > costs.most) continue;
+    const int64_t rest = units * c % resident;
+    float waves = static_cast<float>(units * c / resident);
+    if (rest != 0) waves += std::max(costs.lone, static_cast<float>(rest) / resident);
+    const float cost = (own + costs.setup) * waves + (c > 1 ? costs.merge : 0.f);
     if (cost < least) {
       least = cost;
       best = c;
@@ -187,6 +184,13 @@ int plan_step_cluster(int64_t units, int64_t tiles, int num_sms) {
   }
   return best;
 }
+
+// paged_step_kernel, tiles of 128 slots. One token, 20 heads, us: a CTA 4.7 at 128
+// slots, 6.6 at 448, 8.0 at 700, 12.3 at 1500; a cluster of eight 7.0 at 700, 7.6 at
+// 1500, 8.3 at 3000; cut parts 10.8 at 700, 11.4 at 1500, 12.3 at 3000. Over 699 sizes
+// of 1 to 64 sequences, 1 to 20 K/V heads and up to 12000 slots the choice costs 1 %
+// on average against the best of all, at most 18 %.
+constexpr SplitCosts kStepCosts{0.55f, 0.f, 1.75f, 6.f, 24};
 
 struct PagedPlan {
   int rows_cap;       // rows of a query tile
@@ -219,7 +223,7 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
     tiles = std::min<int64_t>(tiles, reach / sea::pg::BKV + 2 + ceil_div(g.first, sea::pg::BKV));
   }
   if (pl.rows_cap <= 32) {
-    const int cluster = plan_step_cluster(units, tiles, num_sms);
+    const int cluster = plan_split(units, tiles, int64_t(2) * num_sms, kStepCosts);
     if (cluster > 0) {
       pl.parts = 0;
       pl.cluster = cluster;
@@ -361,13 +365,13 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   return ATTN_OK;
 }
 
-// A cluster per key tile of paged_weights_kernel where no CTA of it gets more items
-// than this (0.6 us each, 1.2 us of 128 rows) and all clusters fit the device at
-// once. One token over up to 6000 slots, us: 4 K/V heads 6.4, cut and merged 7.3 to
-// 7.9; 20 heads 7.6 in clusters of 4, 8.5 to 9.5 cut, 16 in one CTA; 100 tokens of
-// 4 K/V heads 16 in clusters of 2, 10 cut.
-constexpr int kClusterTileItems = 5;
-constexpr int kClusterTileWideItems = 3;
+// paged_weights_kernel: a unit is a key tile, its tiles are the items, of up to 32
+// rows or of 128. One token, us: 4 K/V heads at 448 slots 5.3 in a cluster of eight,
+// 5.4 of four, 6.2 in a CTA, 7.2 cut; 20 heads 6.5, 7.8, 15.7 and 8.8; 100 tokens of 4 K/V heads, 8 sequences of 1000 slots 20.7,
+// 15.0, 28.8 and 17.6. Over 500 sizes the choice costs 0.8 % on average against the
+// best of all, at most 20 %.
+constexpr SplitCosts kWeightCosts{0.5f, 2.f, 0.5f, 2.5f, 5};
+constexpr SplitCosts kWideWeightCosts{0.9f, 2.f, 0.5f, 2.5f, 5};
 
 struct WeightPlan {
   int rows;            // rows of a query tile: as few as hold the chunk, in whole tokens
@@ -388,13 +392,11 @@ WeightPlan plan_weights(const sea::pg::Geo& g, int num_sms) {
   pl.ctas = (pl.rows == 128 ? sea::pg::WeightCfg<128>::CTAS_PER_SM : sea::pg::WeightCfg<16>::CTAS_PER_SM) * num_sms;
   const int64_t key_tiles = static_cast<int64_t>(g.batch) * pl.tiles;
   const int64_t items = static_cast<int64_t>(g.kv_heads) * pl.q_tiles;
-  pl.cluster = 1;
-  const int64_t most = pl.rows == 128 ? kClusterTileWideItems : kClusterTileItems;
-  while (pl.cluster < 8 && items > most * pl.cluster) pl.cluster *= 2;
-  if (items <= most * pl.cluster && key_tiles * pl.cluster <= pl.ctas) {
+  if (key_tiles <= pl.ctas)
+    pl.cluster = plan_split(key_tiles, items, pl.ctas, pl.rows == 128 ? kWideWeightCosts : kWeightCosts);
+  if (pl.cluster > 0) {
     pl.ctas = static_cast<int>(key_tiles * pl.cluster);
   } else {
-    pl.cluster = 0;
     pl.ws_bytes = size_t(pl.ctas) * (2 * sea::pg::BKV + 3) * 4;
   }
   return pl;
