@@ -433,6 +433,11 @@ def _paged_mask(window: int, first: int, causal, q_lens, batch: int, device) -> 
     return AttnPagedMask(window, first, 1 if causal else 0, _q_lens_ptr(q_lens, batch, device))
 
 
+def _sizes_fit(t_q: int, n_heads: int) -> None:
+    if not (0 < t_q <= _INT_MAX and 0 < n_heads <= _INT_MAX):
+        raise ValueError(f"t_q and n_heads must be positive and 32-bit, got {t_q} and {n_heads}")
+
+
 def _batch_of(cache: PagedKV, batch: int) -> AttnPagedKV:
     if batch != cache.batch:
         raise ValueError(f"the cache holds {cache.batch} sequences, not {batch}")
@@ -482,12 +487,14 @@ def attn_paged_append(k_new, v_new, cache: PagedKV, batch, t_new, q_lens=None, s
 
 def paged_workspace_size(cache: PagedKV, batch, t_q, n_heads, window=0, first=0, causal=True) -> int:
     """Bytes of workspace attn_paged needs for these sizes on the current device."""
+    _sizes_fit(t_q, n_heads)
     mask = _paged_mask(window, first, causal, None, batch, cache.device)
     return int(load_library().attn_paged_workspace_size(_batch_of(cache, batch), batch, t_q, n_heads, mask))
 
 
 def paged_weights_workspace_size(cache: PagedKV, batch, t_q, n_heads) -> int:
     """Bytes of workspace attn_paged_weights needs for these sizes on the current device."""
+    _sizes_fit(t_q, n_heads)
     return int(load_library().attn_paged_weights_workspace_size(_batch_of(cache, batch), batch, t_q, n_heads))
 
 
@@ -598,6 +605,8 @@ def attn_paged_evict(cache: PagedKV, weights, budget, first=0, recent=0, dst: Op
         dst = cache
     elif dst.device != dev:
         raise ValueError(f"dst is on {dst.device}, the cache on {dev}")
+    if not (0 <= budget <= _INT_MAX and 0 <= first <= _INT_MAX and 0 <= recent <= _INT_MAX):
+        raise ValueError(f"budget, first and recent must be 32-bit and not negative, got {budget}, {first} and {recent}")
     to = _batch_of(dst, batch)
     w_in = _dev_tensor(weights, "weights", torch.float32, (batch, cache.slots), dev)
     if kept is None:

@@ -440,6 +440,24 @@ def test_sinks_far_above_and_below_the_scores(t_q, slots):
     assert (got[:, :64] == 0).all() and ((lse[:, 0] - 300.0).abs() <= 2.0 ** -14).all()  # 2 roundings of 300
 
 
+@pytest.mark.parametrize("bad", [dict(budget=2 ** 32 + 8), dict(budget=33), dict(budget=0), dict(budget=-1), dict(first=2 ** 32 + 1),
+                                 dict(first=-1), dict(recent=2 ** 32), dict(recent=-2)])
+def test_evictions_that_do_not_fit_are_refused(bad):
+    rng = np.random.default_rng(19)
+    cache = make_cache(rng, [20], 1, 16)
+    before = cache.k.clone()
+    w = torch.zeros(1, cache.slots, device="cuda")
+    fits = all(0 <= x < 2 ** 31 for x in bad.values())  # then the library refuses it
+    with pytest.raises(attn.AttnError if fits else ValueError):
+        attn.attn_paged_evict(cache, w, **{"budget": 8, **bad})
+    assert torch.equal(cache.k, before) and cache.lens.item() == 20
+    for t_q, heads in ((2 ** 32 + 1, 1), (1, 2 ** 32 + 1), (0, 1), (1, 0)):
+        with pytest.raises(ValueError):
+            attn.paged_workspace_size(cache, 1, t_q, heads)
+        with pytest.raises(ValueError):
+            attn.paged_weights_workspace_size(cache, 1, t_q, heads)
+
+
 def test_numbers_that_do_not_fit_are_refused():
     rng = np.random.default_rng(18)
     cache = make_cache(rng, [20], 1, 16)
