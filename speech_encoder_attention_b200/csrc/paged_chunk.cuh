@@ -48,10 +48,16 @@ struct ChunkUnit {
 };
 constexpr int kUnitRing = 4;
 
+// Likewise the hole bits of tile t + 4 replace those of tile t when S of tile t + 2
+// is there, whose product waited for the softmax threads to read S of tile t + 1.
+constexpr int kHoleRing = 4;
+
 struct ChunkCfg : fa::CfgT<2> {
   static constexpr int OFF_HOLES = OFF_MISC + 8;
-  static constexpr int OFF_UNITS = OFF_HOLES + 4 * STAGES;
-  static constexpr int SMEM_BYTES = 1024 + OFF_UNITS + kUnitRing * static_cast<int>(sizeof(ChunkUnit));
+  static constexpr int OFF_UNITS = OFF_HOLES + 4 * kHoleRing;
+  static constexpr int OFF_K_EMPTY = OFF_UNITS + kUnitRing * static_cast<int>(sizeof(ChunkUnit));
+  static_assert(OFF_K_EMPTY % 8 == 0, "");
+  static constexpr int SMEM_BYTES = 1024 + OFF_K_EMPTY + 8 * STAGES;
 };
 
 struct ChunkParams {
@@ -117,7 +123,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
   auto q_empty = [&](int i) { return bar0 + 8u * (2 + i); };
   auto k_full = [&](int s) { return bar0 + 8u * (4 + s); };
   auto v_full = [&](int s) { return bar0 + 8u * (4 + ST + s); };
-  auto kv_empty = [&](int s) { return bar0 + 8u * (4 + 2 * ST + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (4 + 2 * ST + s); };
+  auto k_empty = [&](int s) { return sbase + C::OFF_K_EMPTY + 8u * s; };
   const uint32_t s_full = bar0 + 8u * (4 + 3 * ST);
   const uint32_t s_free = s_full + 8u;
   const uint32_t p_full = s_full + 16u;
@@ -140,9 +147,10 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
     for (int s = 0; s < ST; ++s) {
       mbar_init(k_full(s), 1);
       mbar_init(v_full(s), 1);
-      mbar_init(kv_empty(s), 1);
+      mbar_init(v_empty(s), 1);
+      mbar_init(k_empty(s), 1);
     }
-    mbar_init(s_full, 1);
+    mbar_init(s_full, 2);  // S, and what the producer wrote beside K
     mbar_init(s_free, 4);
     mbar_init(p_full, 4);
     mbar_init(o_done, 1);
@@ -168,11 +176,25 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
 
   if (warp == C::PRODUCER_WARP) {
     // ---------------- TMA producer (whole warp: lane i loads page i of a tile) ----------------
+    // K of a tile goes out before V of the tile before it: its stage is free once S
+    // is computed, a softmax earlier than V's.
     const int n_pages = pages_per_tile(g);
     const uint32_t page_bytes = TILE_BYTES / n_pages;
     const uint32_t q_bytes = static_cast<uint32_t>(g.tok_per_tile * g.group) * DH * 2;
     int qn = 0, it = 0;
     ChunkWalk w;
+    PageLoad lv{false, 0};  // of the V tile that is due, its head's column and bytes
+    int v_col = 0;
+    uint32_t v_bytes = 0;
+    auto load_v = [&](int t) {
+      const int st = t % ST;
+      if (!__all_sync(0xffffffffu, mbar_wait(v_empty(st), ((t / ST) & 1) ^ 1u, wc))) return false;
+      if (lane == 0) mbar_arrive_expect_tx(v_full(st), v_bytes);
+      __syncwarp();
+      if (lv.load) tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, v_full(st), v_col, lv.row);
+      return true;
+    };
+    int vn = 0;  // V tiles loaded
     bool more = chunk_start(cp, w), ok = true;
     for (; more; more = ok && chunk_next(cp, w)) {
       if (w.k1 <= w.k0) {  // no row sees anything (whole units only)
@@ -208,19 +230,31 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         PageLoad l{false, 0};
         if (lane < n_pages) l = page_of_tile(g, w.b, w.u, w.u.tile(k), lane);
         const uint32_t loaded = __ballot_sync(0xffffffffu, l.load);
-        ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(st), ((it / ST) & 1) ^ 1u, wc));
+        ok = __all_sync(0xffffffffu, mbar_wait(k_empty(st), ((it / ST) & 1) ^ 1u, wc));
         if (!ok) break;
+        const uint32_t bytes = __popc(loaded) * page_bytes;
         if (lane == 0) {
-          holes[st] = hole_bits(g, loaded);
-          mbar_arrive_expect_tx(k_full(st), __popc(loaded) * page_bytes);
-          mbar_arrive_expect_tx(v_full(st), __popc(loaded) * page_bytes);
+          holes[it % kHoleRing] = hole_bits(g, loaded);
+          mbar_arrive_expect_tx(k_full(st), bytes);
         }
         __syncwarp();
-        if (l.load) {
-          tma_load_2d(sbase + C::OFF_K + st * TILE_BYTES + lane * page_bytes, &tm_k, k_full(st), w.h * DH, l.row);
-          tma_load_2d(sbase + C::OFF_V + st * TILE_BYTES + lane * page_bytes, &tm_v, v_full(st), w.h * DH, l.row);
+        if (l.load) tma_load_2d(sbase + C::OFF_K + st * TILE_BYTES + lane * page_bytes, &tm_k, k_full(st), w.h * DH, l.row);
+        if (it > vn) {
+          ok = load_v(vn);
+          if (!ok) {
+            ++it;
+            break;
+          }
+          ++vn;
         }
+        lv = l;
+        v_col = w.h * DH;
+        v_bytes = bytes;
       }
+    }
+    if (ok && it > vn) {
+      ok = load_v(vn);
+      vn += ok ? 1 : 0;
     }
     if (ok && mbar_wait(q_empty(qn & 1), ((qn >> 1) & 1) ^ 1u, wc) && lane == 0) {  // the end of the walk
       units[qn % kUnitRing].k1 = 0;
@@ -228,10 +262,8 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
     }
     // Let the last copies land before the CTA may exit.
     if (qn > 0) mbar_wait_drain(q_full((qn - 1) & 1), ((qn - 1) >> 1) & 1, p.limit_ns);
-    for (int i = max(0, it - ST); i < it; ++i) {
-      mbar_wait_drain(k_full(i % ST), (i / ST) & 1, p.limit_ns);
-      mbar_wait_drain(v_full(i % ST), (i / ST) & 1, p.limit_ns);
-    }
+    for (int i = max(0, it - ST); i < it; ++i) mbar_wait_drain(k_full(i % ST), (i / ST) & 1, p.limit_ns);
+    for (int i = max(0, vn - ST); i < vn; ++i) mbar_wait_drain(v_full(i % ST), (i / ST) & 1, p.limit_ns);
   } else if (warp == C::MMA_WARP) {
     if (lane == 0) {
       // ---------------- MMA issuer (as in flash_attn_kernel) ----------------
@@ -255,7 +287,7 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
         for (int kk = 0; kk < BKV / 16; ++kk)
           mma_f16_ts(o_t, p_t + kk * 8, vd + kk * 128, idesc_o, (!first || kk > 0) ? 1u : 0u);
         mma_commit(o_done);
-        mma_commit(kv_empty(st));
+        mma_commit(v_empty(st));
         return true;
       };
       while (ok) {
@@ -275,7 +307,9 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
           const uint64_t kd = k_desc0 + st * kTileUnits;
 #pragma unroll
           for (int kk = 0; kk < DH / 16; ++kk) mma_f16_ss(s_t, qd + kk * 2, kd + kk * 2, idesc_s, kk > 0 ? 1u : 0u);
+          mbar_arrive(s_full);
           mma_commit(s_full);
+          mma_commit(k_empty(st));
           if (k > k0 && !issue_pv(it - 1, k == k0 + 1)) {
             ok = false;
             break;
@@ -310,15 +344,11 @@ __global__ void __launch_bounds__(ChunkCfg::THREADS, 2)
       float m_run = -INFINITY, l_run = 0.f;
       for (int k = k0; k < k1; ++k) {
         const int st = it % ST;
-        if (!mbar_wait(k_full(st), (it / ST) & 1, wc)) {  // the producer's hole bits
-          ok = false;
-          break;
-        }
-        const uint32_t hole = holes[st];
         if (!mbar_wait(s_full, it & 1, wc)) {
           ok = false;
           break;
         }
+        const uint32_t hole = holes[it % kHoleRing];
         tc_fence_after();
         float s[BKV];
         {
