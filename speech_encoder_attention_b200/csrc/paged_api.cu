@@ -144,11 +144,10 @@ bool encode_paged_q(CUtensorMap* m, const attn_mat& q, int batch, int t_q, int n
 // is what partials, their merging and the parts' uneven unit ends cost. An SM has two
 // units at a time; an odd one left alone takes kAloneTile of a pair's time. Longest
 // first, causal units of different lengths even out by themselves. 20 heads,
-// us: 8 prompts of 1500 tokens 113 whole, 155 cut; one of 6000 150 and 186; 100
-// tokens after 448 slots 11.7 and 15.7, after 1500 slots 23.0 and 17.5; 4 chunks of
-// 500 tokens at the end of 6000 slots 178 and 132. Over 894 sizes of 40 to 4000
-// tokens and up to 12000 slots the choice costs 0.5 % on average against the better
-// of both, at most 25 %.
+// us: 8 prompts of 1500 tokens 103 whole, 148 cut; one of 6000 143 and 175; 100
+// tokens at the end of 1500 slots 22 and 18; 4 chunks of 500 tokens at the end of 6000
+// slots, 4 K/V heads, 144 and 110. Over 894 sizes of 40 to 4000 tokens and up to 12000
+// slots the choice costs 0.5 % on average against the better of both, at most 18 %.
 constexpr float kAloneTile = 0.7f;
 constexpr float kCutTiles = 5.5f;
 constexpr float kCutShare = 0.1f;

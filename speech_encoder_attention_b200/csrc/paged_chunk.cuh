@@ -10,21 +10,20 @@
 //   warp 4     TMA producer: Q through a 4-D map (column, head, token,
 //              sequence), K and V one copy per page.
 //   warp 5     tcgen05.mma issuer: S = Q K^T, then O += P V.
-// Two ways to deal out the work. With many units (sequence, head, query tile)
-// each CTA walks whole units, the ones at the end of the prompts, which see
-// most, first, every other round in reverse order of the CTAs so that the shares
-// come out even. With few, the key tiles of all units are cut into equal parts as
-// in paged_step_kernel, and paged_combine_kernel merges what was cut.
+// Two ways to deal out the work. Where units (sequence, head, query tile) even out
+// over the SMs each CTA walks whole units, the ones at the end of the prompts, which
+// see most, first, every other round in reverse order of the CTAs. Elsewhere the key
+// tiles of all units are cut into equal parts as in paged_step_kernel, and
+// paged_combine_kernel merges what was cut.
 //
-// Measured on a B200, 20 heads: eight causal prompts of 1500 tokens 113 us = 408
-// TFLOP/s over the visible pairs (46 % of the exponential rate, 21 % of the
-// tensor pipe); four ragged chunks of up to 509 tokens over up to 6007 slots, 4
-// K/V heads, 83 us = 433 TFLOP/s. A key tile takes a softmax thread about 3100
-// cycles, 1024 of them exponentials, and the two CTAs of an SM overlap only in
-// part; leaving out the page and window checks would give 8 %. Slower, each
-// tried: two threads per row with 64 columns each (130 and 104 us), exponentials
-// on half a tile while the other half's max is taken (120 and 87 us), part of
-// the exponentials as polynomials (123 and 88 us at an eighth).
+// Measured on a B200, 20 heads: eight causal prompts of 1500 tokens 103 us = 448
+// TFLOP/s over the visible pairs (exponential unit busy 49 % of the time, tensor
+// pipe 24 %); four ragged chunks of up to 509 tokens over up to 6007 slots, 4
+// K/V heads, 80 us = 449 TFLOP/s. The two CTAs of an SM leave two softmax warps per
+// scheduler, whose chains (scores, max, exponentials, P) overlap only in part.
+// Slower, each tried: two threads per row with 64 columns each (128 and 102 us),
+// exponentials on half a tile while the other half's max is taken, part of the
+// exponentials as polynomials.
 #pragma once
 
 #include "flash_attn.cuh"

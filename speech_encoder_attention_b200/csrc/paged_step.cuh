@@ -15,17 +15,16 @@
 //   warps 0-3   warp w takes slots [32w, 32w + 32) of every key tile with a
 //               running max, sum and output of its own; warp 0 merges the
 //               four at the end of a unit.
-// Two ways to deal out the work. Long caches: the key tiles of all units are cut
+// Two ways to deal out the work. Either the key tiles of all units are cut
 // into equal parts, a CTA for each part and K/V head, two CTAs per SM; units that
-// are cut leave partials that paged_combine_kernel merges. Where a unit has few
-// key tiles: a cluster of up to 8 CTAs per unit, each with an equal run of its
-// tiles, merged through distributed shared memory, with no second launch and no
-// workspace.
+// are cut leave partials that paged_combine_kernel merges. Or a unit has a cluster
+// of 1 to 8 CTAs, each with an equal run of its tiles, merged through distributed
+// shared memory, with no second launch and no workspace.
 //
 // Measured on a B200, 20 heads, one token each: 16 sequences of 3.1 to 8.2
 // thousand slots 80 us = 5.9 TB/s of K and V, 0.90 of the copy rate (its TMA
 // loads alone take 78 us); 48 sequences with a 1024-slot window and 5 K/V heads
-// 17 us = 3.7 TB/s; one sequence 6.5 us at 448 slots, 8.2 us at 3000.
+// 17 us = 3.7 TB/s; one sequence 6.6 us at 448 slots, 8.3 us at 3000.
 #pragma once
 
 #include "paged_common.cuh"
