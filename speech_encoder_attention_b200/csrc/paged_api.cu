@@ -185,8 +185,8 @@ int plan_split(int64_t units, int64_t run, int64_t resident, const SplitCosts& c
 }
 
 // paged_step_kernel, tiles of 128 slots. One token, 20 heads, us: a CTA 4.7 at 128
-// slots, 6.6 at 448, 8.0 at 700, 12.3 at 1500; a cluster of eight 7.0 at 700, 7.6 at
-// 1500, 8.3 at 3000; cut parts 10.8 at 700, 11.4 at 1500, 12.3 at 3000. Over 699 sizes
+// slots, 6.2 at 448, 7.4 at 700, 10.7 at 1500; a cluster of eight 7.0 at 700, 7.6 at
+// 1500, 8.3 at 3000; cut parts 10.9 at 700, 11.6 at 1500, 12.3 at 3000. Over 699 sizes
 // of 1 to 64 sequences, 1 to 20 K/V heads and up to 12000 slots the choice costs 1 %
 // on average against the best of all, at most 18 %.
 constexpr SplitCosts kStepCosts{0.55f, 0.f, 1.75f, 6.f, 24};
@@ -205,7 +205,7 @@ PagedPlan plan_paged(const sea::pg::Geo& g, int num_sms) {
   // Up to 32 rows per K/V head: paged_step_kernel with 16 or 32 rows per tile. 20
   // heads, us: a step over 8000 slots of 16 sequences 106 with 16 rows, 125 with 32;
   // 24 tokens there 132, 175 with paged_chunk_kernel; over 448 slots of one sequence
-  // 6.6, 9.1 and 9.8, 11.0.
+  // 6.2, 9.1 and 9.8, 11.0.
   const int64_t rows = static_cast<int64_t>(t_q) * group;
   pl.rows_cap = rows <= 16 ? 16 : rows <= 32 ? 32 : sea::fa::BQ;
   pl.tok_per_tile = std::max(1, std::min(t_q, pl.rows_cap / group));

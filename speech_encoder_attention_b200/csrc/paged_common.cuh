@@ -321,6 +321,22 @@ __device__ __forceinline__ PageLoad page_of_tile(const Geo& g, int b, const Span
   return l;
 }
 
+// The whole warp: pages of the 32 / n_pages key tiles of a unit from tile k on, in one
+// read of the table; tile k + x's page i is in lane x * n_pages + i. A producer that
+// reads the table tile by tile waits for it before each of its first copies.
+__device__ __forceinline__ PageLoad pages_ahead(const Geo& g, int b, const Span& u, int k, int k1, int n_pages) {
+  const int lane = threadIdx.x & 31;
+  const int kk = k + lane / n_pages;
+  return kk < k1 ? page_of_tile(g, b, u, u.tile(kk), lane & (n_pages - 1)) : PageLoad{false, 0};
+}
+
+// The whole warp: lane i < n_pages gets page i of the x-th of those tiles.
+__device__ __forceinline__ PageLoad page_from(const PageLoad& ahead, int x, int n_pages) {
+  const int lane = threadIdx.x & 31;
+  const int row = __shfl_sync(0xffffffffu, ahead.load ? ahead.row : -1, (x * n_pages + lane) & 31);
+  return PageLoad{lane < n_pages && row >= 0, row};
+}
+
 // Granule bits of the slots the tile's loads leave out, from the ballot of the
 // lanes that load.
 __device__ __forceinline__ uint32_t hole_bits(const Geo& g, uint32_t loaded) {
