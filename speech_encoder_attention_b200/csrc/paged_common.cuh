@@ -118,8 +118,13 @@ __device__ __forceinline__ Span span_of(const Geo& g, const Seq& s, int qt) {
     u.lo = u.hi = 0;
     t_hi = u.t_lo = 0;
   }
+  // Unless causal, the first part may reach past the window part: the tiles behind
+  // the window part that hold first slots are walked with it.
   u.n_first = (u.f + BKV - 1) / BKV;
-  if (t_hi > u.t_lo) u.n_first = min(u.n_first, u.t_lo);
+  if (t_hi > u.t_lo) {
+    t_hi = max(t_hi, u.n_first);
+    u.n_first = min(u.n_first, u.t_lo);
+  }
   u.n = u.n_first + t_hi - u.t_lo;
   return u;
 }

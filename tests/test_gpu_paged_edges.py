@@ -1,0 +1,61 @@
+"""Edges of the paged-cache operators: what a row sees, and values that are not finite."""
+import numpy as np
+import pytest
+import torch
+
+from paged_util import attention64, check_attention, check_weights, make_cache, weights64
+from speech_encoder_attention_b200 import attn
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+@pytest.fixture(autouse=True)
+def no_timeouts():
+    yield
+    st, word = attn.debug_error_word()
+    assert st == attn.ATTN_OK, hex(word)
+
+
+def queries(rng, rows, heads):
+    return torch.from_numpy(rng.standard_normal((rows, heads * 64)).astype(np.float16)).cuda()
+
+
+def i32(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32).cuda()
+
+
+# Not causal, and the first tokens reach past the window of the chunk's earlier rows:
+# key tiles behind the window part hold first tokens too. "cut" ones share the line of tiles.
+OPEN = {
+    "whole": dict(lens=[600, 846], t_q=600, page=16, window=64, first=300),
+    "whole_ragged": dict(lens=[846, 600], t_q=600, page=128, window=86, first=839, q_lens=[583, 600], holes=[(0, 2)]),
+    "cut": dict(lens=[900, 2000], t_q=400, page=64, window=100, first=850),
+    "cut_ragged": dict(lens=[2500, 40, 400], t_q=400, page=256, window=33, first=2000, q_lens=[400, 40, 380]),
+    "more_rows_than_slots": dict(lens=[300, 500], t_q=420, page=32, window=64, first=200),
+    "all_first": dict(lens=[700], t_q=700, page=16, window=30, first=2 ** 31 - 1),
+    "step": dict(lens=[700, 300], t_q=6, page=16, window=30, first=600),
+}
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("name", OPEN)
+def test_first_tokens_past_the_window_are_seen(name, causal):
+    c = OPEN[name]
+    rng = np.random.default_rng(31)
+    batch, t_q, heads, kv_heads = len(c["lens"]), c["t_q"], 4, 2
+    cache = make_cache(rng, c["lens"], kv_heads, c["page"], holes=c.get("holes", ()), garbage=NAN)
+    q, q_lens = queries(rng, batch * t_q, heads), c.get("q_lens")
+    opts = dict(window=c["window"], first=c["first"], causal=causal)
+    if not causal:
+        assert (attn.paged_workspace_size(cache, batch, t_q, heads, **opts) > 0) == ("cut" in name)
+    got, lse = attn.attn_paged(q, cache, batch, t_q, heads, q_lens=i32(q_lens), return_lse=True, **opts)
+    want, want_lse, spread = attention64(q, cache, t_q, heads, q_lens=q_lens, **opts)
+    check_attention(got, lse, want, want_lse, spread, max(c["lens"]))
+    zero = torch.zeros(batch, cache.slots, device="cuda")
+    w = attn.attn_paged_weights(q, cache, lse, batch, t_q, heads, q_lens=i32(q_lens), weights=zero, **opts)
+    check_weights(w, weights64(q, cache, lse, t_q, heads, zero, q_lens=q_lens, **opts), zero)
+    # each row that sees anything hands out a weight of one: 1e-4 per weight, and the sum's own roundings
+    seen = (~torch.isinf(lse)).sum().item()
+    assert abs(w.double().sum().item() - seen) <= 2e-4 * seen
