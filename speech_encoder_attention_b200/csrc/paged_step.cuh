@@ -626,22 +626,22 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const
     if (c8 == 0) sh_ml[x] = make_float2(m, l);
     __syncthreads();
     if (grp != 0) return;
+    // By l, not by m: a group whose scores were all NaN has m = -inf and l = NaN,
+    // and NaN is what comes of it.
     float mx = -INFINITY;
     for (int i = 0; i < groups; ++i) mx = fmaxf(mx, sh_ml[(i << rows_log2) + (x & (block_rows - 1))].x);
     l = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = 0.f;
     const int used = min(groups, c1 - c0 + 1);
-    if (mx != -INFINITY) {
-      for (int i = 0; i < used; ++i) {
-        const int y = (i << rows_log2) + (x & (block_rows - 1));
-        const float2 ml = sh_ml[y];
-        if (!(ml.y != 0.f)) continue;
-        const float wgt = ex2_approx(ml.x - mx);
-        l += ml.y * wgt;
+    for (int i = 0; i < used; ++i) {
+      const int y = (i << rows_log2) + (x & (block_rows - 1));
+      const float2 ml = sh_ml[y];
+      if (ml.y == 0.f) continue;
+      const float wgt = ex2_approx(ml.x - mx);
+      l += ml.y * wgt;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += sh_o[y][c8 + j] * wgt;
-      }
+      for (int j = 0; j < 8; ++j) o[j] += sh_o[y][c8 + j] * wgt;
     }
     m = mx;
   }

@@ -59,3 +59,43 @@ def test_first_tokens_past_the_window_are_seen(name, causal):
     # each row that sees anything hands out a weight of one: 1e-4 per weight, and the sum's own roundings
     seen = (~torch.isinf(lse)).sum().item()
     assert abs(w.double().sum().item() - seen) <= 2e-4 * seen
+
+
+# Few slots per sequence: a CTA per unit; more: clusters of CTAs; many: units cut into parts.
+@pytest.mark.parametrize("slots", [None, 1500, 14000])
+@pytest.mark.parametrize("t_q", [1, 16, 100])
+def test_a_nan_query_comes_back_as_nan(t_q, slots):
+    """A NaN in one row's query for one head makes NaN of that output and lse, and of no other, on every path."""
+    rng = np.random.default_rng(32)
+    cache = make_cache(rng, [1000, 300], 2, 16, slots=slots)
+    assert slots != 14000 or attn.paged_workspace_size(cache, 2, t_q, 4) > 0
+    q = queries(rng, 2 * t_q, 4)
+    clean, clean_lse = attn.attn_paged(q, cache, 2, t_q, 4, return_lse=True)
+    row, head = t_q // 2, 3
+    q[row, head * 64 + 5] = NAN
+    sinks = torch.zeros(4, device="cuda")
+    got, lse = attn.attn_paged(q, cache, 2, t_q, 4, return_lse=True)
+    sunk, sunk_lse = attn.attn_paged(q, cache, 2, t_q, 4, sinks=sinks, return_lse=True)
+    for o, l in ((got, lse), (sunk, sunk_lse)):
+        assert torch.isnan(o[row, head * 64:]).all() and torch.isnan(l[row, head])
+        assert torch.isnan(o).sum() == 64 and torch.isnan(l).sum() == 1
+    got[row, head * 64:] = clean[row, head * 64:]
+    lse[row, head] = clean_lse[row, head]
+    assert torch.equal(got, clean) and torch.equal(lse, clean_lse)
+
+
+@pytest.mark.parametrize("slots", [None, 1500, 14000])
+@pytest.mark.parametrize("t_q", [1, 16, 100])
+def test_a_cache_of_nan_keys_comes_back_as_nan(t_q, slots):
+    """Every key of one head of one sequence is NaN, or only those of its last key tile."""
+    rng = np.random.default_rng(33)
+    cache = make_cache(rng, [1000, 300], 2, 16, slots=slots)
+    q = queries(rng, 2 * t_q, 4)
+    clean, clean_lse = attn.attn_paged(q, cache, 2, t_q, 4, return_lse=True)
+    for begin in (896, 0):
+        for i in range(begin // 16, 63):
+            cache.k[int(cache.table[0, i]) * 16:(int(cache.table[0, i]) + 1) * 16, 64:] = NAN
+        got, lse = attn.attn_paged(q, cache, 2, t_q, 4, return_lse=True)
+        assert torch.isnan(got[:t_q, 128:]).all() and torch.isnan(lse[:t_q, 2:]).all()
+        assert torch.equal(got[:t_q, :128], clean[:t_q, :128]) and torch.equal(got[t_q:], clean[t_q:])
+        assert torch.equal(lse[:t_q, :2], clean_lse[:t_q, :2]) and torch.equal(lse[t_q:], clean_lse[t_q:])
