@@ -33,6 +33,8 @@
 // at 55 % of the exponential rate.
 #pragma once
 
+#include <cfloat>
+
 #include "flash_attn.cuh"
 #include "paged_common.cuh"
 
@@ -138,6 +140,17 @@ __device__ __forceinline__ void entry_at(const WeightParams& p, Entry& e, int b,
   e.seen = tokens_seeing(g, e.s, tile * BKV, (tile + 1) * BKV);
   e.chunks = (e.seen.hi - e.seen.lo + g.tok_per_tile - 1) / g.tok_per_tile;
   e.items = e.chunks * g.kv_heads;
+}
+
+// Whether a row that sees the slot, of tokens `mine` of sequence b, has a NaN for its
+// normaliser. Asked only of infinite sums.
+__device__ __forceinline__ bool nan_among(const WeightParams& p, int b, const Tokens& mine) {
+  const float* row = p.lse + (static_cast<int64_t>(b) * p.g.t_q + mine.lo) * p.g.n_heads;
+  const float* end = row + static_cast<int64_t>(mine.hi - mine.lo) * p.g.n_heads;
+  bool any = false;
+#pragma unroll 1
+  for (; row < end; ++row) any |= *row != *row;
+  return any;
 }
 
 // The next entry with items. Sequences end at their last slot, and no row sees
@@ -355,7 +368,9 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     const uint32_t page_bytes = TILE_BYTES / n_pages;
     const uint32_t q_bytes = static_cast<uint32_t>(g.tok_per_tile * g.group) * DH * 2;
     // Normalisers of an item's rows, negated, read an item ahead: each costs a
-    // round trip to L2. -inf takes a row's weight to zero.
+    // round trip to L2. -inf takes a row's weight to zero. A NaN is handed over as
+    // the largest number, which makes infinities of the slots that the row sees and
+    // leaves the others, whose scores are -inf by then, alone.
     constexpr int LANE_ROWS = (N + 31) / 32;
     const int q_rows = g.tok_per_tile * g.group;
     int row_tok[LANE_ROWS], row_head[LANE_ROWS];  // this lane's rows of a query tile
@@ -406,7 +421,8 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
 #pragma unroll
       for (int x = 0; x < LANE_ROWS; ++x)
         if (32 * x + lane < N)
-          lse_ring[st * N + 32 * x + lane] = norm[x] == -INFINITY ? -INFINITY : -norm[x] * kLog2e;
+          lse_ring[st * N + 32 * x + lane] =
+              norm[x] != norm[x] ? FLT_MAX : norm[x] == -INFINITY ? -INFINITY : -norm[x] * kLog2e;
       read_norms(i + 1);
       __syncwarp();
       if (lane == 0) {
@@ -521,7 +537,10 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       __syncwarp();
       if (lane == 0) mbar_arrive(q_empty(qs));
     }
-    if (page < 0 || page >= g.num_pages) sum = 0.f;
+    if (page < 0 || page >= g.num_pages)
+      sum = 0.f;
+    else if (sum == INFINITY && nan_among(p, w.e.b, mine))
+      sum = NAN;
     if constexpr (C::SPLIT == 2) {
       if (!ok) break;
       if (half == 1) {

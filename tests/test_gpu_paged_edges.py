@@ -9,6 +9,7 @@ from speech_encoder_attention_b200 import attn
 pytestmark = pytest.mark.gpu
 
 NAN = float("nan")
+INF = float("inf")
 
 
 @pytest.fixture(autouse=True)
@@ -99,3 +100,60 @@ def test_a_cache_of_nan_keys_comes_back_as_nan(t_q, slots):
         assert torch.isnan(got[:t_q, 128:]).all() and torch.isnan(lse[:t_q, 2:]).all()
         assert torch.equal(got[:t_q, :128], clean[:t_q, :128]) and torch.equal(got[t_q:], clean[t_q:])
         assert torch.equal(lse[:t_q, :2], clean_lse[:t_q, :2]) and torch.equal(lse[t_q:], clean_lse[t_q:])
+
+
+def slots_seen(cache, b, t_q, row, window, first, causal):
+    """Which of sequence b's slots its row sees, [slots] bool."""
+    kv = int(cache.lens[b])
+    p = row + kv - t_q
+    j = torch.arange(cache.slots, device="cuda")
+    see = (j < kv) & (j <= p) if causal else j < kv
+    if window:
+        see &= ((j - p).abs() < window) | (j < first)
+    table = cache.table[b].repeat_interleave(cache.page_size)
+    return see & (table >= 0) & (table < cache.k.shape[0] // cache.page_size)
+
+
+# Few slots per sequence: a CTA or a cluster per key tile; many: shares of the line of items.
+@pytest.mark.parametrize("slots", [None, 80000])
+@pytest.mark.parametrize("window,first,causal", [(0, 0, True), (50, 3, True), (40, 130, False)])
+@pytest.mark.parametrize("t_q", [1, 5, 14, 90, 200])
+def test_a_nan_lse_reaches_only_the_slots_its_row_sees(t_q, window, first, causal, slots):
+    rng = np.random.default_rng(34)
+    batch, heads = 2, 4
+    cache = make_cache(rng, [300, 250], 2, 16, slots=slots, holes=[(0, 4)], garbage=NAN)
+    q = queries(rng, batch * t_q, heads)
+    opts = dict(window=window, first=first, causal=causal)
+    assert (attn.paged_weights_workspace_size(cache, batch, t_q, heads) > 0) == (slots is not None)
+    _, lse, _ = attention64(q, cache, t_q, heads, **opts)
+    lse = lse.float().contiguous()
+    w_in = torch.from_numpy(rng.random((batch, cache.slots)).astype(np.float32)).cuda()
+    clean = attn.attn_paged_weights(q, cache, lse, batch, t_q, heads, weights=w_in, **opts)
+    assert torch.isfinite(clean).all()
+    for rows in ([0], [t_q // 2, t_q - 1]):
+        bad = lse.clone()
+        hit = torch.zeros(cache.slots, dtype=torch.bool, device="cuda")
+        for n, i in enumerate(rows):
+            bad[i, (1 + 2 * n) % heads] = NAN
+            hit |= slots_seen(cache, 0, t_q, i, window, first, causal)
+        got = attn.attn_paged_weights(q, cache, bad, batch, t_q, heads, weights=w_in, **opts)
+        assert torch.isnan(got[0, hit]).all()
+        assert torch.equal(got[0, ~hit], clean[0, ~hit]) and torch.equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("slots", [None, 80000])
+@pytest.mark.parametrize("t_q", [1, 90])
+def test_weights_that_overflow_are_infinite(t_q, slots):
+    """An lse far below its row's scores is no NaN: e^(s - lse) is infinite where the row sees a slot."""
+    rng = np.random.default_rng(36)
+    cache = make_cache(rng, [300, 250], 2, 16, slots=slots)
+    q = queries(rng, 2 * t_q, 4)
+    lse = torch.full((2 * t_q, 4), 8.0, device="cuda")
+    clean = attn.attn_paged_weights(q, cache, lse, 2, t_q, 4, window=50)
+    lse[t_q + t_q // 2, 1] = -1000.0
+    got = attn.attn_paged_weights(q, cache, lse, 2, t_q, 4, window=50)
+    hit = slots_seen(cache, 1, t_q, t_q // 2, 50, 0, True)
+    assert (got[1, hit] == INF).all() and torch.equal(got[1, ~hit], clean[1, ~hit]) and torch.equal(got[0], clean[0])
+    lse[t_q + t_q // 2, 0] = NAN  # of another head
+    got = attn.attn_paged_weights(q, cache, lse, 2, t_q, 4, window=50)
+    assert torch.isnan(got[1, hit]).all() and torch.equal(got[1, ~hit], clean[1, ~hit])
