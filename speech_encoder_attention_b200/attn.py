@@ -392,6 +392,25 @@ class PagedKV(namedtuple("PagedKV", "k v table lens page_size n_kv_heads batch s
                                                         rows // page_size, page_size, per_seq, n_kv_heads))
         return tuple.__new__(cls, (k, v, table, lens, page_size, n_kv_heads, batch, per_seq * page_size, dev, c))
 
+    # Every way to another PagedKV goes through the checks: c holds addresses.
+
+    def __getnewargs__(self):
+        return tuple(self[:6])
+
+    def _replace(self, **changes):
+        """This cache with some of k, v, table, lens, page_size and n_kv_heads exchanged, checked as a new one."""
+        given = dict(zip(self._fields, self[:6]))
+        other = [name for name in changes if name not in given]
+        if other:
+            raise ValueError(f"a PagedKV is made of {', '.join(given)}, not of {', '.join(other)}")
+        return type(self)(**{**given, **changes})
+
+    __replace__ = _replace
+
+    @classmethod
+    def _make(cls, iterable):
+        raise TypeError("a PagedKV is made from its tensors: PagedKV(k, v, table, lens, page_size, n_kv_heads)")
+
 
 _INT_MAX = 2 ** 31 - 1
 _PAGED_KV = struct.Struct("@QqQqQQiiii")  # the fields of AttnPagedKV, in order
