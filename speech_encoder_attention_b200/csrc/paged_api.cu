@@ -319,7 +319,6 @@ attn_status launch_paged(attn_mat q, attn_paged_kv cache, int32_t batch, int32_t
   p.rows_cap = pl.rows_cap;
   p.parts = pl.parts;
   p.cluster = pl.cluster;
-  p.least = 1;
   p.err = dev->err;
   p.limit_ns = sea::kDefaultTimeoutNs;
   using sea::pg::StepCfg;
@@ -396,7 +395,7 @@ WeightPlan plan_weights(const sea::pg::Geo& g, int num_sms) {
   if (pl.cluster > 0) {
     pl.ctas = static_cast<int>(key_tiles * pl.cluster);
   } else {
-    pl.ws_bytes = size_t(pl.ctas) * (2 * sea::pg::BKV + 3) * 4;
+    pl.ws_bytes = size_t(pl.ctas) * (2 * sea::pg::BKV + 2) * 4;
   }
   return pl;
 }

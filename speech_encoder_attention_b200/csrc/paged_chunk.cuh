@@ -91,7 +91,7 @@ __device__ __forceinline__ bool chunk_start(const ChunkParams& p, ChunkWalk& w) 
   const Geo& g = p.s.g;
   if (p.cut) {
     w.h = blockIdx.x % g.kv_heads;
-    return walk_start(g, w, blockIdx.x / g.kv_heads, p.s.parts, p.s.least);
+    return walk_start(g, w, blockIdx.x / g.kv_heads, p.s.parts);
   }
   w.round = 0;
   w.unit = blockIdx.x;

@@ -191,10 +191,9 @@ __device__ __forceinline__ int tiles_before_q(const Geo& g, const Seq& s, int qt
   return sum;
 }
 
-// Tiles per part: an equal share, at least `least`.
-__device__ __forceinline__ long long share_of(long long total, int parts, int least) {
-  const long long per = (total + parts - 1) / parts;
-  return per < least ? least : per;
+// Tiles per part: an equal share, and one of an empty line, which others divide by.
+__device__ __forceinline__ long long share_of(long long total, int parts) {
+  return max(1ll, (total + parts - 1) / parts);
 }
 
 // One part, unit by unit. Every warp of the CTA walks the same steps.
@@ -218,13 +217,13 @@ __device__ __forceinline__ void walk_cut(const Geo& g, Walk& w, int k0) {
 }
 
 // One warp; returns false if the part is empty.
-__device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int part, int parts, int least) {
+__device__ __forceinline__ bool walk_start(const Geo& g, Walk& w, int part, int parts) {
   const int lane = threadIdx.x & 31;
   // Up to 32 sequences: a lane each, looked at once.
   const bool once = g.q_tiles <= 4 && g.batch <= 32;
   const int lane_tiles = once && lane < g.batch ? tiles_of_seq(g, lane) : 0;
   const long long total = once ? __reduce_add_sync(0xffffffffu, lane_tiles) : tiles_before(g, g.batch);
-  const long long per = share_of(total, parts, least);
+  const long long per = share_of(total, parts);
   w.begin = w.pos = per * part;
   w.end = min(total, w.pos + per);
   if (w.pos >= w.end) return false;

@@ -51,7 +51,6 @@ struct StepParams {
   int rows_cap;
   int parts;         // the line of key tiles is cut into this many; 0: a cluster per unit
   int cluster;       // CTAs of that cluster, at most 8
-  int least;         // fewest key tiles per part
   uint32_t* err;
   uint64_t limit_ns;
 };
@@ -147,7 +146,7 @@ __global__ void __launch_bounds__(StepCfg<MT>::THREADS, 2)
   Walk w;
   bool any;
   if constexpr (CUT) {
-    any = walk_start(g, w, blockIdx.x / g.kv_heads, p.parts, p.least);
+    any = walk_start(g, w, blockIdx.x / g.kv_heads, p.parts);
   } else {
     const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
     w.b = unit / g.kv_heads;
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS, 4) paged_combine_kernel(const
     all += sum_all[i];
     before += sum_before[i];
   }
-  const long long per = share_of(all, p.parts, p.least);
+  const long long per = share_of(all, p.parts);
   const int c0 = static_cast<int>(before / per);
   const int c1 = rows > 0 ? static_cast<int>((before + u.n - 1) / per) : c0;
   const bool c0_first = before == per * c0;

@@ -51,8 +51,8 @@ struct WeightParams {
   int tiles;           // key tiles per sequence, by the table's size
   int cluster;         // 0: shares of the line; else so many CTAs, a cluster, per key tile
   float* ws_sum;       // [CTAs][2][128] sums of cut key tiles: one begun earlier, one that goes on
-  int* ws_state;       // [CTAs][3]: the tile begun earlier ends or passes here; the entry of the one
-                       // that goes on (-1: none), and in how many more shares
+  int* ws_state;       // [CTAs][2]: the entry of the one that goes on (-1: none), and in how many
+                       // more shares
   uint32_t* err;
   uint64_t limit_ns;
 };
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
     const int t = threadIdx.x & (BKV - 1);
     float* half_sum = reinterpret_cast<float*>(smem + C::OFF_HALF);
     int n = 0, entry_n = 0;
-    int begun = 0, on = -1, more = 0;  // for the merge: see ws_state
+    int on = -1, more = 0;  // for the merge: see ws_state
     // For rank 0, where the last query tile was: its products are done by then.
     float* total = reinterpret_cast<float*>(smem + C::OFF_Q);
     if (p.cluster > 1 && half == 0 && w.left <= 0) total[t] = 0.f;
@@ -567,15 +567,12 @@ __global__ void __launch_bounds__(WeightCfg<N>::THREADS, WeightCfg<N>::CTAS_PER_
       if (starts) {
         on = w.e.b * p.tiles + w.e.tile;
         more = static_cast<int>((w.e.items - w.i1 + per - 1) / per);
-      } else {
-        begun = 1;
       }
     }
     } while (ok && w.next(p));
     if (threadIdx.x == 0 && p.cluster == 0) {
-      p.ws_state[3 * blockIdx.x] = begun;
-      p.ws_state[3 * blockIdx.x + 1] = on;
-      p.ws_state[3 * blockIdx.x + 2] = more;
+      p.ws_state[2 * blockIdx.x] = on;
+      p.ws_state[2 * blockIdx.x + 1] = more;
     }
     // Slots of key tiles that no row sees keep their weights.
     if (p.w_in != p.w_out && half == 0) {
@@ -623,9 +620,9 @@ __global__ void __launch_bounds__(BKV) paged_weights_merge_kernel(const WeightPa
   griddep_wait();
   griddep_launch_dependents();
   const int c = blockIdx.x, t = threadIdx.x;
-  const int entry = p.ws_state[3 * c + 1];
+  const int entry = p.ws_state[2 * c];
   if (entry < 0) return;
-  const int more = p.ws_state[3 * c + 2];
+  const int more = p.ws_state[2 * c + 1];
   const int b = entry / p.tiles, j = (entry - b * p.tiles) * BKV + t;
   float v = p.ws_sum[(2 * static_cast<int64_t>(c) + 1) * BKV + t];
 #pragma unroll 4
