@@ -157,3 +157,27 @@ def test_weights_that_overflow_are_infinite(t_q, slots):
     lse[t_q + t_q // 2, 0] = NAN  # of another head
     got = attn.attn_paged_weights(q, cache, lse, 2, t_q, 4, window=50)
     assert torch.isnan(got[1, hit]).all() and torch.equal(got[1, ~hit], clean[1, ~hit])
+
+
+@pytest.mark.parametrize("slots", [None, 1500, 14000])
+@pytest.mark.parametrize("t_q", [12, 100, 300])
+def test_a_nan_key_of_a_chunk_stays_with_the_rows_that_see_it(t_q, slots):
+    """The key of one of the chunk's own tokens, causal and with a window: earlier rows and later ones are clean."""
+    rng = np.random.default_rng(37)
+    cache = make_cache(rng, [400, 300], 2, 16, slots=slots)
+    q = queries(rng, 2 * t_q, 4)
+    clean, clean_lse = attn.attn_paged(q, cache, 2, t_q, 4, window=5, return_lse=True)
+    row = t_q // 2
+    slot = row + 400 - t_q
+    cache.k[int(cache.table[0, slot // 16]) * 16 + slot % 16, :64] = NAN
+    got, lse = attn.attn_paged(q, cache, 2, t_q, 4, window=5, return_lse=True)
+    w = attn.attn_paged_weights(q, cache, lse, 2, t_q, 4, window=5)
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[row:row + 5, :2] = True
+    assert torch.isnan(lse[hit]).all() and torch.equal(lse[~hit], clean_lse[~hit])
+    assert torch.isnan(got.view(-1, 4, 64)[hit]).all()
+    assert torch.equal(got.view(-1, 4, 64)[~hit], clean.view(-1, 4, 64)[~hit])
+    seen = torch.zeros_like(w, dtype=torch.bool)
+    for i in range(row, row + 5):
+        seen[0] |= slots_seen(cache, 0, t_q, i, 5, 0, True)
+    assert torch.isnan(w[seen]).all() and torch.isfinite(w[~seen]).all()
