@@ -319,6 +319,10 @@ attn_status attn_paged_append(attn_mat k_new, attn_mat v_new, attn_paged_kv cach
  * A row that sees nothing (padding rows i >= Q too) is zero with lse = -inf.
  * Precision as in attn_forward: fp32 scores, max, sum and output, softmax
  * weights rounded to fp16 for the value product, the output rounded once.
+ * A NaN in a query or a key comes back as NaN from the rows and heads that see
+ * it, and from no others. A NaN or an infinity in a value does too, but may also
+ * make NaN of rows of the same chunk that do not see its slot: their weight of
+ * zero does not silence it.
  * workspace: at least attn_paged_workspace_size(...) bytes, 16-byte aligned
  * (NULL with 0 bytes where that is 0: short caches and windows); a smaller one
  * returns ATTN_ERR_INVALID. Calls that may run at the same time need a
@@ -336,8 +340,9 @@ size_t attn_paged_workspace_size(attn_paged_kv cache, int32_t batch, int32_t t_q
 /*
  * attn_paged_weights -- the attention weight each slot receives from a chunk
  *   w_out[b, j] = w_in[b, j] + sum_{i, h : j in A_i} e^{s_ij - lse_ih}
- * with attn_paged's s, A_i and lse (a row with lse = -inf has no weight). The
- * sums are fp32, added in a fixed order.
+ * with attn_paged's s, A_i and lse (a row of finite scores with lse = -inf has no
+ * weight; a NaN lse makes NaN of the slots that its row sees, and of no others).
+ * The sums are fp32, added in a fixed order.
  *   lse    [batch*t_q, n_heads] fp32
  *   w_in   [batch, pages_per_seq*page_size] fp32, or NULL for zeros
  *   w_out  the same shape; w_in itself, or not overlapping it

@@ -364,9 +364,10 @@ class PagedKV(namedtuple("PagedKV", "k v table lens page_size n_kv_heads batch s
     in use, new tokens included. Slot j of sequence b is row
     table[b, j // page_size] * page_size + j % page_size.
 
-    The tensors are checked here, once, and cannot be exchanged; what they hold
-    may change at any time (a captured graph follows table and lens). batch,
-    slots (per sequence), device and c (the C structure) follow from them."""
+    The tensors are checked here, once, and cannot be exchanged (_replace makes
+    another PagedKV, checked anew); what they hold may change at any time (a
+    captured graph follows table and lens). batch, slots (per sequence), device
+    and c (the C structure) follow from them."""
     __slots__ = ()
 
     def __new__(cls, k, v, table, lens, page_size: int, n_kv_heads: int):

@@ -184,7 +184,7 @@ int plan_split(int64_t units, int64_t run, int64_t resident, const SplitCosts& c
   return best;
 }
 
-// paged_step_kernel, tiles of 128 slots. One token, 20 heads, us: a CTA 4.7 at 128
+// paged_step_kernel, tiles of 128 slots. One token, 20 heads, 64-slot pages, us: a CTA 4.7 at 128
 // slots, 6.2 at 448, 7.4 at 700, 10.7 at 1500; a cluster of eight 7.0 at 700, 7.6 at
 // 1500, 8.3 at 3000; cut parts 10.9 at 700, 11.6 at 1500, 12.3 at 3000. Over 699 sizes
 // of 1 to 64 sequences, 1 to 20 K/V heads and up to 12000 slots the choice costs 1 %

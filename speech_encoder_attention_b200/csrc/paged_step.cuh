@@ -25,7 +25,10 @@
 // Measured on a B200, 20 heads, one token each: 16 sequences of 3.1 to 8.2
 // thousand slots 80 us = 5.9 TB/s of K and V, 0.90 of the copy rate (its TMA
 // loads alone take 78 us); 48 sequences with a 1024-slot window and 5 K/V heads
-// 16 us = 3.9 TB/s; one sequence 6.2 us at 448 slots, 8.3 us at 3000.
+// 16 us = 3.9 TB/s; one sequence in 64-slot pages 5.9 us at 448 slots, 8.0 us at
+// 3000 (in 16-slot pages, with eight copies for K and for V per tile, 7.1 and 8.6).
+// Registers: 16 rows fit without spills; 32 rows spill 232 bytes a thread where the
+// line is cut and 36 bytes where it is not.
 #pragma once
 
 #include "paged_common.cuh"

@@ -30,7 +30,8 @@
 // Measured on a B200, 20 heads: one token of each of 16 sequences of 3.1 to 8.2
 // thousand slots 52 us = 4.6 TB/s (the loads run at 6.5 TB/s; 10 us are launch,
 // the first tile's latency and the merge), 4 causal prompts of 1500 tokens 52 us
-// at 55 % of the exponential rate.
+// at 55 % of the exponential rate (64 scores per thread, of which 216 bytes are
+// spilled at 96 registers).
 #pragma once
 
 #include <cfloat>
